@@ -178,6 +178,167 @@ AROPS_API arops_status arops_mrope_kv_append(const void* q, const void* k, const
                                              arops_dtype dtype, void* stream);
 
 /*
+ * Paged KV cache.  A pool of pages holds the keys and values of many sequences;
+ * a block table names, in order, the pages of each sequence: position p of
+ * sequence s lives in page block_table[s * max_pages + p / page_size], slot
+ * p % page_size.  The pages hold their slots per head, as the dense cache of
+ * arops_mrope_kv_append does: that cache is the special case of one page per
+ * cache row with page_size = max_seq.
+ */
+typedef struct {
+    void* k_pages;       /* [num_pages, n_kv_heads, page_size, head_dim] dtype, device */
+    void* v_pages;       /* likewise; another buffer */
+    int64_t num_pages;   /* 1 <= num_pages <= 2^31 - 1 */
+    int32_t page_size;   /* slots of a page, >= 1 (any size; multiples of 16 are fastest) */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    arops_dtype dtype;   /* of the pages and of every other tensor of the call */
+} arops_paged_cache;
+
+/*
+ * A ragged batch over a paged cache.  The query tokens of the n_seqs sequences
+ * lie one after another; sequence s owns tokens q_start[s] .. q_start[s+1] - 1
+ * and kv_lens[s] cache positions INCLUDING those of its query tokens, which are
+ * its last ones: token t of sequence s is at position
+ *   i = kv_lens[s] - (q_start[s+1] - t).
+ * All arrays are int32 on the device and are read when the kernel runs, so a
+ * captured call follows their contents.  Tokens at and behind q_start[n_seqs]
+ * belong to no sequence (a padded batch): nothing of theirs is written.
+ * Block-table entries behind a sequence's last page are never looked at.
+ * Whatever the arrays hold, nothing out of range is read or written: tokens
+ * that no pair 0 <= q_start[s] <= q_start[s+1] <= tokens covers belong to no
+ * sequence; a length above max_pages * page_size counts as that, and a page
+ * outside the pool is not written, and read as zeros, both with
+ * AROPS_DEVICE_ERR_BAD_INDEX set in the device error word.  q_start that is
+ * not non-decreasing gives unspecified results within those bounds.
+ */
+typedef struct {
+    const int32_t* q_start;     /* [n_seqs + 1], non-decreasing from 0 */
+    const int32_t* kv_lens;     /* [n_seqs] */
+    const int32_t* block_table; /* [n_seqs, max_pages] */
+    int32_t n_seqs;
+    int32_t max_pages;
+} arops_paged_batch;
+
+/*
+ * M-RoPE fused with the append to a paged KV cache, for prompts and for single
+ * tokens.  For every token of the batch, in one pass: q and k are normalised
+ * per head where a weight is given (RMSNorm over head_dim: gamma * x /
+ * sqrt(mean(x^2) + eps)), rotated as arops_mrope_qk rotates them (all in fp32,
+ * rounded once), q into q_out and k into the token's cache slot; v is copied
+ * into its slot.
+ *   q [tokens, n_q_heads, head_dim], k and v [tokens, n_kv_heads, head_dim]:
+ *     each token's heads are dense; the tokens are q_stride, k_stride and
+ *     v_stride elements apart (slices of one packed projection, for instance).
+ *   q_out [tokens, n_q_heads, head_dim], q_out_stride elements a token; may be
+ *     q with q's stride.
+ *   gamma_q, gamma_k [head_dim] dtype or NULL (no norm); eps >= 0 is used only
+ *     with a weight.
+ *   pos [3, tokens] int32, sections, theta, head_dim: as for arops_mrope_qk.
+ * Where the position in the cache (from the batch) and the rotation's position
+ * ids differ, as they do behind an image or audio grid, both are honoured.
+ * A token whose position or page is out of range has its q rotated and its
+ * slot left out (AROPS_DEVICE_ERR_BAD_INDEX).  Slots that no token names keep
+ * their bits.  Two tokens naming one slot race.
+ */
+AROPS_API arops_status arops_mrope_paged_append(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, void* q_out, int64_t q_out_stride, const arops_paged_cache* cache,
+    const arops_paged_batch* batch, const void* gamma_q, const void* gamma_k, float eps,
+    const int32_t* pos, int64_t tokens, int32_t n_q_heads, const int32_t* sections, float theta,
+    void* stream);
+
+/*
+ * What happens to a score between the product and the softmax.  For the query
+ * at position i and the key at position j of its sequence, in this order:
+ *   s = scale * (q_i . k_j)
+ *   softcap > 0:      s = softcap * tanh(s / softcap)
+ *   slopes != NULL:   s = s - slopes[head] * |i - j|
+ * and key j < kv_len is seen by query i if
+ *   (j <= i  or  j < bidir_lens[s])  and  (window == 0  or  j > i - window).
+ * bidir_lens lets a sequence's first positions (a prompt) be seen by all its
+ * queries, earlier ones included; NULL is a causal mask.
+ */
+typedef struct {
+    float scale;               /* finite; 1/sqrt(head_dim) usually */
+    float softcap;             /* finite, >= 0; 0: no cap */
+    int32_t window;            /* >= 0 positions, the query's own included; 0: no limit */
+    const float* slopes;       /* [n_q_heads] float32 device array, or NULL */
+    const int32_t* bidir_lens; /* [n_seqs] int32 device array, or NULL */
+} arops_attention_options;
+
+/*
+ * Attention over a paged KV cache, for prompts, chunks of prompts and single
+ * tokens in one batch:
+ *   out[t, h] = sum_j softmax_j(s_ij) v_j      over the keys j that t sees
+ * with key/value head h * n_kv_heads / n_q_heads (n_q_heads is a multiple of
+ * n_kv_heads).  A token that sees no key gets zeros.
+ *   q   [tokens, n_q_heads, head_dim], q_stride elements a token (heads dense)
+ *   out [tokens, n_q_heads, head_dim] dense; not q and not part of the cache
+ *   head_dim <= 256 (bf16) or 128 (fp32); n_seqs, n_q_heads <= 65535.
+ * Scores, softmax statistics and sums are fp32.  In bf16 the weights of the
+ * second product are rounded to bf16, as q, k and v are; in fp32 both products
+ * run on the tensor cores with every operand split into two tf32 parts (about
+ * 21 bits).  The values of slots at and behind a sequence's length, and of
+ * pages that it does not name, never reach the result, whatever they hold;
+ * values inside the length are expected to be finite (a NaN or an infinity
+ * there may reach queries that do not see it).
+ *   workspace   device scratch of at least arops_attention_workspace() bytes
+ *               (16-byte aligned, caller-owned).  It starts with 16 KiB of
+ *               arrival counters that must be zero when a call begins: clear
+ *               them once, with arops_attention_prepare; every call leaves them
+ *               zero again, for any later call of either attention operator.
+ *               Two calls in flight at once must not share one workspace (nor
+ *               may two captured graphs that can be replayed at once); calls
+ *               of one stream may.
+ * The work (all keys of all rows) is cut into equal shares, one a CTA, from the
+ * lengths on the device: no host plan, no dependence on the order of arrival,
+ * and the same lengths give the same bits.
+ */
+AROPS_API arops_status arops_attention_workspace(int64_t tokens, int32_t n_q_heads,
+                                                 int32_t head_dim, size_t* bytes);
+AROPS_API arops_status arops_attention_prepare(void* workspace, size_t workspace_bytes,
+                                               void* stream);
+AROPS_API arops_status arops_paged_attention(const void* q, int64_t q_stride, void* out,
+                                             const arops_paged_cache* cache,
+                                             const arops_paged_batch* batch,
+                                             const arops_attention_options* options,
+                                             int64_t tokens, int32_t n_q_heads, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
+ * Groups of sequences that share a prompt: the sequences of group g are
+ * group_start[g] .. group_start[g+1] - 1, their first prefix_lens[g] positions
+ * lie in the pages of prefix_table's row g, once for all of them.  Sequences
+ * at and behind group_start[n_groups] belong to no group: they are left out.
+ */
+typedef struct {
+    const int32_t* group_start;  /* [n_groups + 1], non-decreasing from 0 */
+    const int32_t* prefix_lens;  /* [n_groups] */
+    const int32_t* prefix_table; /* [n_groups, max_prefix_pages] */
+    int32_t n_groups;
+    int32_t max_prefix_pages;
+} arops_prefix_groups;
+
+/*
+ * Decode attention of candidates that share a prompt (several continuations of
+ * one text, as in the five candidates generated together): one query token per
+ * sequence, whose keys are its group's prefix_lens[g] positions and then its
+ * own kv_lens[s] positions, from batch->block_table.  The query stands at the
+ * last of them, position prefix_lens[g] + kv_lens[s] - 1.  The prefix is read
+ * once for the rows of a group that fit one tile, not once per sequence.
+ *   q, out [n_seqs, n_q_heads, head_dim] as for arops_paged_attention
+ *   batch->q_start is ignored (may be NULL); options->bidir_lens must be NULL.
+ * Options, workspace, limits, rounding and malformed entries are as for
+ * arops_paged_attention; kv_lens[s] may be 0, and so may prefix_lens[g].
+ */
+AROPS_API arops_status arops_shared_prefix_attention(
+    const void* q, int64_t q_stride, void* out, const arops_paged_cache* cache,
+    const arops_paged_batch* batch, const arops_prefix_groups* groups,
+    const arops_attention_options* options, int32_t n_q_heads, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
  * SwiGLU activation ("SwiGLU" in the Triton kernel-fusion post, section 3):
  *   out = silu(gate) * up,  silu(g) = g / (1 + e^-g), computed in fp32.
  *   gate, up, out: [rows, inter] dtype, separate tensors (out may be gate or up).

@@ -35,6 +35,7 @@ _BUILD = os.path.join(_HERE, "_build")
 _c_double_p = ctypes.POINTER(ctypes.c_double)
 _c_u16_p = ctypes.POINTER(ctypes.c_uint16)
 _c_i32_p = ctypes.POINTER(ctypes.c_int32)
+_c_i64_p = ctypes.POINTER(ctypes.c_int64)
 
 
 def lib_path(mutant: int = 0, omp: bool = False) -> str:
@@ -98,6 +99,11 @@ class Oracle:
         L.oracle_mrope_qk.argtypes = [_c_double_p, _c_double_p, _c_double_p, _c_double_p,
                                       _c_i32_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
                                       ctypes.c_int, _c_i32_p, ctypes.c_double]
+        L.oracle_attention.argtypes = [
+            _c_double_p, _c_double_p, _c_double_p, _c_double_p, _c_i64_p, _c_i64_p, _c_i64_p,
+            _c_i64_p, _c_i64_p, _c_double_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+            ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_double, ctypes.c_double,
+            ctypes.c_double, ctypes.c_double, _c_double_p, _c_double_p]
         L.oracle_swiglu.argtypes = [_c_double_p, _c_double_p, _c_double_p, ctypes.c_int64]
         L.oracle_layernorm.argtypes = [_c_double_p, _c_double_p, _c_double_p, _c_double_p,
                                        ctypes.c_int64, ctypes.c_int64, ctypes.c_double]
@@ -251,6 +257,104 @@ class Oracle:
             _ptr(pos, _c_i32_p), _ptr(loc, _c_i32_p), tokens, hq, hk, d, rows, max_seq,
             _ptr(sec, _c_i32_p), float(theta), _ptr(k_rot, _c_double_p))
         return q_out, kc, vc
+
+    # -- paged cache ------------------------------------------------------------
+    @staticmethod
+    def _slots(table_row, length: int, num_pages: int, page_size: int) -> np.ndarray:
+        """Slot (page * page_size + slot) of positions 0..length; -1 where the
+        table names a page outside the pool."""
+        p = np.arange(length)
+        page = np.asarray(table_row, dtype=np.int64)[p // page_size] if length else p
+        return np.where((page >= 0) & (page < num_pages), page * page_size + p % page_size, -1)
+
+    def mrope_paged_append(self, q, k, v, pos, q_start, kv_lens, block_table, k_pages, v_pages,
+                           sections=(24, 20, 20), theta: float = 1e6, gamma_q=None, gamma_k=None,
+                           eps: float = 1e-6, q_out=None):
+        """Per-head RMSNorm where a weight is given, then mrope_kv_append with
+        every token's slot taken from the batch.  Tokens of no sequence keep
+        q_out's values.  Returns (q_out, k_pages', v_pages') in fp64."""
+        q, k = _f64(q), _f64(k)
+        tokens = q.shape[0]
+        start, lens, table = (np.asarray(a) for a in (q_start, kv_lens, block_table))
+        pages, page_size = k_pages.shape[0], k_pages.shape[2]
+        loc = np.full((2, tokens), -1, dtype=np.int32)
+        owned = np.zeros(tokens, dtype=bool)
+        for s in range(lens.size):
+            for t in range(start[s], start[s + 1]):
+                owned[t] = True
+                p = lens[s] - (start[s + 1] - t)
+                if 0 <= p < table.shape[1] * page_size:
+                    loc[:, t] = table[s, p // page_size], p % page_size
+        if gamma_q is not None:
+            q = self.rmsnorm(q.reshape(-1, q.shape[2]), gamma_q, eps).reshape(q.shape)
+        if gamma_k is not None:
+            k = self.rmsnorm(k.reshape(-1, k.shape[2]), gamma_k, eps).reshape(k.shape)
+        out, kp, vp = self.mrope_kv_append(q, k, v, pos, loc, k_pages, v_pages, sections, theta)
+        if q_out is not None:
+            out[~owned] = _f64(q_out)[~owned]
+        assert pages == kp.shape[0]
+        return out, kp, vp
+
+    def _attention(self, q, k_pages, v_pages, slots, of, at, bidir, scale, softcap, window, slopes,
+                   c_dot, c_abs):
+        """slots: a list of slot lists; of[t] the list of token t (-1: none);
+        at[t], bidir[t] its position and its sequence's bidirectional length."""
+        q, kp, vp = _f64(q), _f64(k_pages), _f64(v_pages)
+        tokens, hq, d = q.shape
+        hk, page_size = kp.shape[1], kp.shape[2]
+        begin = np.cumsum([0] + [len(x) for x in slots])
+        flat = np.ascontiguousarray(np.concatenate([*slots, [0]]), dtype=np.int64)
+        of = np.asarray(of)
+        off = np.ascontiguousarray(np.where(of >= 0, begin[of], 0), dtype=np.int64)
+        size = np.array([len(x) for x in slots] + [0], dtype=np.int64)
+        n = np.ascontiguousarray(np.where(of >= 0, size[of], 0), dtype=np.int64)
+        at = np.ascontiguousarray(at, dtype=np.int64)
+        bidir = np.ascontiguousarray(bidir, dtype=np.int64)
+        sl = None if slopes is None else _f64(slopes)
+        out, mass, err = np.empty_like(q), np.empty_like(q), np.empty_like(q)
+        self._lib.oracle_attention(
+            _ptr(q, _c_double_p), _ptr(kp, _c_double_p), _ptr(vp, _c_double_p),
+            _ptr(out, _c_double_p), _ptr(flat, _c_i64_p), _ptr(off, _c_i64_p), _ptr(n, _c_i64_p),
+            _ptr(at, _c_i64_p), _ptr(bidir, _c_i64_p),
+            None if sl is None else _ptr(sl, _c_double_p), tokens, hq, hk, d, page_size, window,
+            d ** -0.5 if scale is None else scale, softcap, c_dot, c_abs, _ptr(mass, _c_double_p),
+            _ptr(err, _c_double_p))
+        return out, mass, err
+
+    def paged_attention(self, q, k_pages, v_pages, q_start, kv_lens, block_table, scale=None,
+                        softcap=0.0, window=0, slopes=None, bidir_lens=None, c_dot=0.0, c_abs=0.0):
+        """Returns (out, mass, err): see oracle_attention.  Tokens of no
+        sequence come back as zeros."""
+        start, lens, table = (np.asarray(a) for a in (q_start, kv_lens, block_table))
+        tokens = q.shape[0]
+        slots, of = [], np.full(tokens, -1)
+        at, bidir = np.zeros(tokens), np.zeros(tokens)
+        for s in range(lens.size):
+            n = int(np.clip(lens[s], 0, table.shape[1] * k_pages.shape[2]))
+            slots.append(self._slots(table[s], n, k_pages.shape[0], k_pages.shape[2]))
+            for t in range(start[s], start[s + 1]):
+                of[t], at[t] = s, n - (start[s + 1] - t)
+                bidir[t] = 0 if bidir_lens is None else int(bidir_lens[s])
+        return self._attention(q, k_pages, v_pages, slots, of, at, bidir, scale, softcap, window,
+                               slopes, c_dot, c_abs)
+
+    def shared_prefix_attention(self, q, k_pages, v_pages, group_start, prefix_lens, prefix_table,
+                                kv_lens, block_table, scale=None, softcap=0.0, window=0,
+                                slopes=None, c_dot=0.0, c_abs=0.0):
+        """Returns (out, mass, err); sequences of no group come back as zeros."""
+        start, plens, ptab, lens, table = (np.asarray(a) for a in (
+            group_start, prefix_lens, prefix_table, kv_lens, block_table))
+        tokens, (pages, _, page_size, _) = q.shape[0], k_pages.shape
+        slots, of, at = [np.empty(0, dtype=np.int64)] * tokens, np.full(tokens, -1), np.zeros(tokens)
+        for g in range(plens.size):
+            n = int(np.clip(plens[g], 0, ptab.shape[1] * page_size))
+            prompt = self._slots(ptab[g], n, pages, page_size)
+            for s in range(start[g], start[g + 1]):
+                m = int(np.clip(lens[s], 0, table.shape[1] * page_size))
+                slots[s] = np.concatenate([prompt, self._slots(table[s], m, pages, page_size)])
+                of[s], at[s] = s, n + m - 1
+        return self._attention(q, k_pages, v_pages, slots, of, at, np.zeros(tokens), scale, softcap,
+                               window, slopes, c_dot, c_abs)
 
     def swiglu(self, gate, up) -> np.ndarray:
         gate = _f64(gate)

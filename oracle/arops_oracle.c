@@ -34,6 +34,7 @@
  */
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #ifndef ORACLE_MUTANT
 #define ORACLE_MUTANT 0
@@ -365,6 +366,100 @@ void oracle_mrope_kv_append(const double* q, const double* k, const double* v, d
 #endif
             }
         }
+    }
+}
+
+/* ------------------------------------------------------------------------- */
+/* Attention over listed cache slots.  Token t attends to the len[t] positions */
+/* whose slots (page * page_size + slot, or -1 for a page outside the pool:    */
+/* zeros) start at slots[off[t]]; it stands at position at[t].  Key j is seen  */
+/* if (j <= at or j < bidir) and (window == 0 or j > at - window); the score   */
+/* is scale * q.k, capped by cap * tanh(s / cap) for cap > 0, less             */
+/* slope * |at - j|.  Two passes: maximum, then weights.                       */
+/* mass (may be NULL) gets sum_j p_j |v_j| (p normalised); err (may be NULL)   */
+/* gets sum_j p_j d_j |v_j| + |out| sum_j p_j d_j, what errors of size         */
+/* d_j = c_dot * scale * sum|q||k_j| + c_abs * (1 + |s_j| + bias_j + cap)      */
+/* in the scores can change the result by, to first order.                     */
+/* ------------------------------------------------------------------------- */
+void oracle_attention(const double* q, const double* k_pages, const double* v_pages, double* out,
+                      const int64_t* slots, const int64_t* off, const int64_t* len,
+                      const int64_t* at, const int64_t* bidir, const double* slopes,
+                      int64_t tokens, int hq, int hk, int head_dim, int64_t page_size,
+                      int64_t window, double scale, double cap, double c_dot, double c_abs,
+                      double* mass, double* err)
+{
+    OMP_ROWS
+    for (int64_t t = 0; t < tokens; ++t) {
+        double* s = malloc(sizeof(double) * (size_t)(2 * len[t] + 1));
+        double* dlt = s + len[t];
+        for (int h = 0; h < hq; ++h) {
+            const double* qh = q + (t * hq + h) * (int64_t)head_dim;
+            double* oh = out + (t * hq + h) * (int64_t)head_dim;
+            double* mh = mass ? mass + (t * hq + h) * (int64_t)head_dim : NULL;
+            double* eh = err ? err + (t * hq + h) * (int64_t)head_dim : NULL;
+            int kvh = h / (hq / hk);
+            double m = -INFINITY, sum = 0.0, dsum = 0.0;
+            for (int d = 0; d < head_dim; ++d) {
+                oh[d] = 0.0;
+                if (mh)
+                    mh[d] = 0.0;
+                if (eh)
+                    eh[d] = 0.0;
+            }
+            for (int64_t j = 0; j < len[t]; ++j) {
+                int seen = (j <= at[t] || j < bidir[t]) && (window == 0 || j > at[t] - window);
+                s[j] = -INFINITY;
+                if (!seen)
+                    continue;
+                int64_t slot = slots[off[t] + j];
+                double dot = 0.0, mag = 0.0;
+                if (slot >= 0) {
+                    const double* kj = k_pages + ((slot / page_size * hk + kvh) * page_size +
+                                                  slot % page_size) * head_dim;
+                    for (int d = 0; d < head_dim; ++d) {
+                        dot += qh[d] * kj[d];
+                        mag += fabs(qh[d] * kj[d]);
+                    }
+                }
+                double x = dot * scale;
+                if (cap > 0.0)
+                    x = cap * tanh(x / cap);
+                double bias = slopes ? slopes[h] * fabs((double)(at[t] - j)) : 0.0;
+                dlt[j] = c_dot * fabs(scale) * mag + c_abs * (1.0 + fabs(x) + fabs(bias) + cap);
+                s[j] = x - bias;
+                if (s[j] > m)
+                    m = s[j];
+            }
+            if (m == -INFINITY)
+                continue; /* no key is seen: zeros */
+            for (int64_t j = 0; j < len[t]; ++j) {
+                if (s[j] == -INFINITY)
+                    continue;
+                double p = exp(s[j] - m);
+                int64_t slot = slots[off[t] + j];
+                sum += p;
+                dsum += p * dlt[j];
+                if (slot < 0)
+                    continue;
+                const double* vj = v_pages + ((slot / page_size * hk + kvh) * page_size +
+                                              slot % page_size) * head_dim;
+                for (int d = 0; d < head_dim; ++d) {
+                    oh[d] += p * vj[d];
+                    if (mh)
+                        mh[d] += p * fabs(vj[d]);
+                    if (eh)
+                        eh[d] += p * dlt[j] * fabs(vj[d]);
+                }
+            }
+            for (int d = 0; d < head_dim; ++d) {
+                oh[d] /= sum;
+                if (mh)
+                    mh[d] /= sum;
+                if (eh)
+                    eh[d] = eh[d] / sum + fabs(oh[d]) * dsum / sum;
+            }
+        }
+        free(s);
     }
 }
 

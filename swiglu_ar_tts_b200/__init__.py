@@ -19,6 +19,8 @@ import torch
 
 __all__ = [
     "rmsnorm", "add_rmsnorm", "layernorm", "add_layernorm", "mrope_qk", "mrope_kv_append",
+    "mrope_paged_append", "paged_attention", "shared_prefix_attention",
+    "attention_workspace", "attention_prepare",
     "swiglu", "set_pdl",
     "set_streaming", "set_topk_cluster", "topk_sample", "topk_sample_workspace", "topk_sample_prepare",
     "device_errors", "launch_count",
@@ -37,6 +39,30 @@ _lib = None
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+
+
+class _PagedCache(ctypes.Structure):
+    """arops_paged_cache"""
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("num_pages", _i64), ("page_size", _i32),
+                ("n_kv_heads", _i32), ("head_dim", _i32), ("dtype", ctypes.c_int)]
+
+
+class _PagedBatch(ctypes.Structure):
+    """arops_paged_batch"""
+    _fields_ = [("q_start", _vp), ("kv_lens", _vp), ("block_table", _vp), ("n_seqs", _i32),
+                ("max_pages", _i32)]
+
+
+class _AttentionOptions(ctypes.Structure):
+    """arops_attention_options"""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", _i32),
+                ("slopes", _vp), ("bidir_lens", _vp)]
+
+
+class _PrefixGroups(ctypes.Structure):
+    """arops_prefix_groups"""
+    _fields_ = [("group_start", _vp), ("prefix_lens", _vp), ("prefix_table", _vp),
+                ("n_groups", _i32), ("max_prefix_pages", _i32)]
 
 
 class ArOpsError(RuntimeError):
@@ -87,6 +113,21 @@ def lib() -> ctypes.CDLL:
         L.arops_topk_sample.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i32, ctypes.c_float,
                                         ctypes.c_int, _vp, ctypes.c_size_t, _vp]
         L.arops_topk_sample.restype = ctypes.c_int
+        cache, batch = ctypes.POINTER(_PagedCache), ctypes.POINTER(_PagedBatch)
+        options, groups = ctypes.POINTER(_AttentionOptions), ctypes.POINTER(_PrefixGroups)
+        L.arops_mrope_paged_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, cache,
+                                               batch, _vp, _vp, ctypes.c_float, _vp, _i64, _i32,
+                                               ctypes.POINTER(_i32), ctypes.c_float, _vp]
+        L.arops_attention_workspace.argtypes = [_i64, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
+        L.arops_attention_prepare.argtypes = [_vp, ctypes.c_size_t, _vp]
+        L.arops_paged_attention.argtypes = [_vp, _i64, _vp, cache, batch, options, _i64, _i32, _vp,
+                                            ctypes.c_size_t, _vp]
+        L.arops_shared_prefix_attention.argtypes = [_vp, _i64, _vp, cache, batch, groups, options,
+                                                    _i32, _vp, ctypes.c_size_t, _vp]
+        for fn in ("arops_mrope_paged_append", "arops_attention_workspace",
+                   "arops_attention_prepare", "arops_paged_attention",
+                   "arops_shared_prefix_attention"):
+            getattr(L, fn).restype = ctypes.c_int
         L.arops_set_pdl.argtypes = [ctypes.c_int]
         L.arops_set_pdl.restype = ctypes.c_int
         L.arops_set_streaming.argtypes = [ctypes.c_int]
@@ -281,6 +322,223 @@ def mrope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torc
             v_cache.data_ptr(), pos.data_ptr(), cache_loc.data_ptr(), tokens, hq, hk, d,
             k_cache.shape[0], k_cache.shape[2], sec, float(theta), code, _stream(q)))
     return q_out
+
+
+def _token_stride(name: str, t: torch.Tensor) -> int:
+    """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
+    heads are dense (a slice of a packed projection is)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if t.numel() == 0:
+        return h * d
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}'s heads must be dense (strides {t.stride()})")
+    if n > 1 and t.stride(0) < h * d:
+        raise ValueError(f"{name}'s tokens overlap (strides {t.stride()})")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _check_device(named) -> None:
+    """Every (name, tensor) lies on the first one's CUDA device."""
+    dev = None
+    for name, t in named:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+
+
+def _check_int32(name: str, t: torch.Tensor, shape) -> None:
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be int32 {list(shape)}")
+
+
+def _paged_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, heads_dim: int) -> _PagedCache:
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [pages, n_kv_heads, page_size, head_dim]")
+    if k_pages.shape[3] != heads_dim:
+        raise ValueError(f"the pages hold heads of {k_pages.shape[3]}, q heads of {heads_dim}")
+    n, hk, page, d = k_pages.shape
+    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, page, hk, d,
+                       _dtype_code(k_pages, v_pages))
+
+
+def mrope_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                       q_start: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
+                       k_pages: torch.Tensor, v_pages: torch.Tensor, sections=(24, 20, 20),
+                       theta: float = 1e6, gamma_q: torch.Tensor | None = None,
+                       gamma_k: torch.Tensor | None = None, eps: float = 1e-6,
+                       q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Normalise (where a weight [D] is given) and rotate q [T, Hq, D] into
+    ``q_out`` (default in place) and k [T, Hk, D] into its slot of the paged
+    cache k_pages/v_pages [pages, Hk, page_size, D], and copy v into its slot.
+    Sequence s owns tokens q_start[s]..q_start[s+1] and, after the call,
+    kv_lens[s] cache positions in the pages block_table[s]; its tokens are the
+    last of them.  q, k and v may be slices of one packed projection (dense
+    heads, any token stride).  Returns ``q_out``."""
+    if q_out is None:
+        q_out = q
+    _check_device((("q", q), ("k", k), ("v", v), ("pos", pos), ("q_start", q_start),
+                   ("kv_lens", kv_lens), ("block_table", block_table), ("k_pages", k_pages),
+                   ("v_pages", v_pages), ("q_out", q_out)))
+    weights = tuple((n, g) for n, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k))
+                    if g is not None)
+    _check_tensors((("pos", pos), ("q_start", q_start), ("kv_lens", kv_lens),
+                    ("block_table", block_table), ("k_pages", k_pages), ("v_pages", v_pages))
+                   + weights)
+    strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
+    tokens, hq, d = q.shape
+    cache = _paged_cache(k_pages, v_pages, d)
+    if k.shape != (tokens, cache.n_kv_heads, d) or v.shape != k.shape or q_out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    if any(g.shape != (d,) for _, g in weights):
+        raise ValueError("gamma_q and gamma_k must be [head_dim]")
+    n_seqs = kv_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [n_seqs, max_pages]")
+    _check_int32("pos", pos, (3, tokens))
+    _check_int32("q_start", q_start, (n_seqs + 1,))
+    _check_int32("kv_lens", kv_lens, (n_seqs,))
+    _check_int32("block_table", block_table, (n_seqs, block_table.shape[1]))
+    _dtype_code(q, k, v, q_out, k_pages, *(g for _, g in weights))
+    batch = _PagedBatch(q_start.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n_seqs,
+                        block_table.shape[1])
+    sec = (_i32 * 3)(*[int(s) for s in sections])
+    with torch.cuda.device(q.device):
+        _check(lib().arops_mrope_paged_append(
+            q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
+            q_out.data_ptr(), strides[3], ctypes.byref(cache), ctypes.byref(batch),
+            None if gamma_q is None else gamma_q.data_ptr(),
+            None if gamma_k is None else gamma_k.data_ptr(), float(eps), pos.data_ptr(), tokens,
+            hq, sec, float(theta), _stream(q)))
+    return q_out
+
+
+def attention_workspace(tokens: int, n_q_heads: int, head_dim: int) -> int:
+    """Bytes of device workspace that paged_attention and
+    shared_prefix_attention need for this many query tokens."""
+    n = ctypes.c_size_t(0)
+    _check(lib().arops_attention_workspace(tokens, n_q_heads, head_dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+def attention_prepare(workspace: torch.Tensor) -> torch.Tensor:
+    """Clears the arrival counters of a new attention workspace (a uint8 device
+    tensor) on the current stream; needed once, before its first use."""
+    _check_tensors((("workspace", workspace),))
+    with torch.cuda.device(workspace.device):
+        _check(lib().arops_attention_prepare(workspace.data_ptr(),
+                                             workspace.numel() * workspace.element_size(),
+                                             _stream(workspace)))
+    return workspace
+
+
+def _attention_args(q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes,
+                    bidir_lens, workspace, out, extra):
+    """Checks and arguments that both attention operators share."""
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    tokens, hq, d = q.shape
+    if out is None:
+        out = torch.empty(tokens, hq, d, dtype=q.dtype, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(attention_workspace(tokens, hq, d), dtype=torch.uint8,
+                                device=q.device)
+        if q.is_cuda:
+            attention_prepare(workspace)
+    optional = tuple((n, t) for n, t in (("slopes", slopes), ("bidir_lens", bidir_lens))
+                     if t is not None)
+    dense = (("k_pages", k_pages), ("v_pages", v_pages), ("kv_lens", kv_lens),
+             ("block_table", block_table), ("workspace", workspace), ("out", out)
+             ) + optional + extra
+    _check_device((("q", q),) + dense)
+    _check_tensors(dense)
+    stride = _token_stride("q", q)
+    cache = _paged_cache(k_pages, v_pages, d)
+    _dtype_code(q, out, k_pages)
+    n_seqs = kv_lens.numel()
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [n_seqs, max_pages]")
+    _check_int32("kv_lens", kv_lens, (n_seqs,))
+    _check_int32("block_table", block_table, (n_seqs, block_table.shape[1]))
+    if slopes is not None and (slopes.dtype != torch.float32 or tuple(slopes.shape) != (hq,)):
+        raise ValueError("slopes must be float32 [n_q_heads]")
+    if bidir_lens is not None:
+        _check_int32("bidir_lens", bidir_lens, (n_seqs,))
+    options = _AttentionOptions(float(d ** -0.5 if scale is None else scale), float(softcap),
+                                int(window), None if slopes is None else slopes.data_ptr(),
+                                None if bidir_lens is None else bidir_lens.data_ptr())
+    batch = _PagedBatch(None, kv_lens.data_ptr(), block_table.data_ptr(), n_seqs,
+                        block_table.shape[1])
+    return stride, cache, batch, options, workspace, out
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                    q_start: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
+                    scale: float | None = None, softcap: float = 0.0, window: int = 0,
+                    slopes: torch.Tensor | None = None, bidir_lens: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [T, Hq, D] (dense heads, any token stride) over the paged
+    cache [pages, Hk, page_size, D]: sequence s owns tokens
+    q_start[s]..q_start[s+1], the last of its kv_lens[s] positions, in the pages
+    block_table[s].  Causal; the first bidir_lens[s] positions are seen by all
+    of the sequence's queries; ``window`` > 0 hides keys that far back;
+    ``softcap`` > 0 caps scores by a tanh; ``slopes`` [Hq] subtracts
+    slope * distance.  ``scale`` defaults to D ** -0.5.  ``workspace`` is a
+    uint8 tensor of attention_workspace() bytes, cleared once
+    (attention_prepare); allocated and cleared here if omitted."""
+    stride, cache, batch, options, workspace, out = _attention_args(
+        q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes, bidir_lens,
+        workspace, out, (("q_start", q_start),))
+    _check_int32("q_start", q_start, (batch.n_seqs + 1,))
+    batch.q_start = q_start.data_ptr()
+    with torch.cuda.device(q.device):
+        _check(lib().arops_paged_attention(
+            q.data_ptr(), stride, out.data_ptr(), ctypes.byref(cache), ctypes.byref(batch),
+            ctypes.byref(options), q.shape[0], q.shape[1], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(q)))
+    return out
+
+
+def shared_prefix_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                            group_start: torch.Tensor, prefix_lens: torch.Tensor,
+                            prefix_table: torch.Tensor, kv_lens: torch.Tensor,
+                            block_table: torch.Tensor, scale: float | None = None,
+                            softcap: float = 0.0, window: int = 0,
+                            slopes: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Decode attention of candidates that share a prompt: query s of q
+    [n_seqs, Hq, D] sees the prefix_lens[g] positions of its group (sequences
+    group_start[g]..group_start[g+1], pages prefix_table[g]) and then its own
+    kv_lens[s] positions (pages block_table[s]), at whose end it stands.
+    Options, workspace and ``out`` as for paged_attention."""
+    stride, cache, batch, options, workspace, out = _attention_args(
+        q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes, None,
+        workspace, out, (("group_start", group_start), ("prefix_lens", prefix_lens),
+                         ("prefix_table", prefix_table)))
+    if q.shape[0] != batch.n_seqs:
+        raise ValueError("q must hold one token per sequence")
+    n_groups = prefix_lens.numel()
+    if prefix_table.dim() != 2:
+        raise ValueError("prefix_table must be int32 [n_groups, max_prefix_pages]")
+    _check_int32("group_start", group_start, (n_groups + 1,))
+    _check_int32("prefix_lens", prefix_lens, (n_groups,))
+    _check_int32("prefix_table", prefix_table, (n_groups, prefix_table.shape[1]))
+    groups = _PrefixGroups(group_start.data_ptr(), prefix_lens.data_ptr(),
+                           prefix_table.data_ptr(), n_groups, prefix_table.shape[1])
+    with torch.cuda.device(q.device):
+        _check(lib().arops_shared_prefix_attention(
+            q.data_ptr(), stride, out.data_ptr(), ctypes.byref(cache), ctypes.byref(batch),
+            ctypes.byref(groups), ctypes.byref(options), q.shape[1], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(q)))
+    return out
 
 
 def swiglu(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:

@@ -7,6 +7,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "paged.cuh"
 
 namespace arops {
 
@@ -271,6 +272,297 @@ AROPS_API arops_status arops_mrope_kv_append(const void* q, const void* k, const
     x.cache_rows = cache_rows;
     x.max_seq = max_seq;
     return from_cuda(launch_mrope_append(a, x, dtype, static_cast<cudaStream_t>(stream)), name);
+}
+
+}  // extern "C"
+
+namespace {
+
+// A pool of pages: its sizes, and (when it holds anything) its pointers.
+arops_status check_cache(const char* name, const arops_paged_cache* c, int32_t max_head_dim)
+{
+    if (!c)
+        return fail(AROPS_ERR_INVALID, "%s: cache is null", name);
+    if (!valid_dtype(c->dtype))
+        return fail(AROPS_ERR_INVALID, "%s: unknown dtype %d", name, (int)c->dtype);
+    if (c->num_pages < 1 || c->page_size < 1 || c->n_kv_heads < 0 || c->head_dim < 1)
+        return fail(AROPS_ERR_INVALID,
+                    "%s: bad cache shape [%lld pages, %d heads, %d slots, %d values]", name,
+                    (long long)c->num_pages, (int)c->n_kv_heads, (int)c->page_size,
+                    (int)c->head_dim);
+    if (c->num_pages > INT32_MAX)
+        return fail(AROPS_ERR_UNSUPPORTED, "%s: %lld pages > 2^31 - 1", name,
+                    (long long)c->num_pages);
+    if (c->head_dim > max_head_dim)
+        return fail(AROPS_ERR_UNSUPPORTED, "%s: head_dim %d > %d", name, (int)c->head_dim,
+                    (int)max_head_dim);
+    if (c->n_kv_heads > 0 && (!c->k_pages || !c->v_pages))
+        return fail(AROPS_ERR_INVALID, "%s: null page pool", name);
+    if (c->n_kv_heads > 0 && c->k_pages == c->v_pages)
+        return fail(AROPS_ERR_INVALID, "%s: k_pages and v_pages are one buffer", name);
+    return AROPS_OK;
+}
+
+arops_status check_batch(const char* name, const arops_paged_batch* b, const arops_paged_cache* c,
+                         int64_t tokens, bool needs_q_start)
+{
+    if (!b)
+        return fail(AROPS_ERR_INVALID, "%s: batch is null", name);
+    if (tokens < 0 || b->n_seqs < 0 || b->max_pages < 0)
+        return fail(AROPS_ERR_INVALID, "%s: negative size", name);
+    if (tokens > INT32_MAX || (int64_t)b->max_pages * c->page_size > INT32_MAX)
+        return fail(AROPS_ERR_UNSUPPORTED, "%s: tokens and max_pages * page_size must be < 2^31",
+                    name);
+    if (tokens == 0 || b->n_seqs == 0)
+        return AROPS_OK;
+    if ((needs_q_start && !b->q_start) || !b->kv_lens || (b->max_pages > 0 && !b->block_table))
+        return fail(AROPS_ERR_INVALID, "%s: null batch array", name);
+    return AROPS_OK;
+}
+
+// Distance between two tokens of a [tokens, heads, head_dim] operand whose
+// heads are dense.
+arops_status check_stride(const char* name, const char* what, int64_t stride, int64_t heads,
+                          int64_t head_dim)
+{
+    if (stride < heads * head_dim)
+        return fail(AROPS_ERR_INVALID, "%s: %s_stride %lld < heads * head_dim = %lld", name, what,
+                    (long long)stride, (long long)(heads * head_dim));
+    return AROPS_OK;
+}
+
+arops_status check_workspace(const char* name, const void* workspace, size_t bytes, size_t need)
+{
+    if (!workspace)
+        return fail(AROPS_ERR_INVALID, "%s: workspace is null", name);
+    if (bytes < need)
+        return fail(AROPS_ERR_INVALID, "%s: workspace of %zu bytes < %zu needed", name, bytes,
+                    need);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+        return fail(AROPS_ERR_INVALID, "%s: workspace not 16-byte aligned", name);
+    return AROPS_OK;
+}
+
+// The checks and the launch that the two attention operators share.
+arops_status attention_entry(const char* name, const void* q, int64_t q_stride, void* out,
+                             const arops_paged_cache* cache, const arops_paged_batch* batch,
+                             const arops_prefix_groups* groups,
+                             const arops_attention_options* opt, int64_t tokens,
+                             int32_t n_q_heads, void* workspace, size_t workspace_bytes,
+                             void* stream)
+{
+    arops_status st = check_cache(name, cache, 256);
+    if (st != AROPS_OK)
+        return st;
+    if (cache->dtype == AROPS_F32 && cache->head_dim > 128)
+        return fail(AROPS_ERR_UNSUPPORTED, "%s: head_dim %d > 128 in fp32", name,
+                    (int)cache->head_dim);
+    st = check_batch(name, batch, cache, tokens, groups == nullptr);
+    if (st != AROPS_OK)
+        return st;
+    if (batch->n_seqs > 65535 || n_q_heads > 65535)
+        return fail(AROPS_ERR_UNSUPPORTED, "%s: supported n_seqs <= 65535, n_q_heads <= 65535",
+                    name);
+    if (n_q_heads < 1 || cache->n_kv_heads < 1 || n_q_heads % cache->n_kv_heads != 0)
+        return fail(AROPS_ERR_INVALID, "%s: n_q_heads %d is not a multiple of n_kv_heads %d", name,
+                    (int)n_q_heads, (int)cache->n_kv_heads);
+    if (!opt)
+        return fail(AROPS_ERR_INVALID, "%s: options is null", name);
+    if (!isfinite(opt->scale) || !isfinite(opt->softcap) || opt->softcap < 0.0f ||
+        opt->window < 0)
+        return fail(AROPS_ERR_INVALID,
+                    "%s: scale and softcap must be finite, softcap and window >= 0", name);
+    st = check_stride(name, "q", q_stride, n_q_heads, cache->head_dim);
+    if (st != AROPS_OK)
+        return st;
+    if (groups) {
+        if (groups->n_groups < 0 || groups->max_prefix_pages < 0)
+            return fail(AROPS_ERR_INVALID, "%s: negative size", name);
+        if (opt->bidir_lens)
+            return fail(AROPS_ERR_INVALID, "%s: bidir_lens must be null", name);
+        if (((int64_t)groups->max_prefix_pages + batch->max_pages) * cache->page_size > INT32_MAX)
+            return fail(AROPS_ERR_UNSUPPORTED,
+                        "%s: (max_prefix_pages + max_pages) * page_size must be < 2^31", name);
+        if (groups->n_groups > batch->n_seqs)
+            return fail(AROPS_ERR_INVALID, "%s: more groups (%d) than sequences (%d)", name,
+                        (int)groups->n_groups, (int)batch->n_seqs);
+    }
+    if (tokens == 0 || batch->n_seqs == 0 || (groups && groups->n_groups == 0))
+        return ok();
+    if (groups && (!groups->group_start || !groups->prefix_lens ||
+                   (groups->max_prefix_pages > 0 && !groups->prefix_table)))
+        return fail(AROPS_ERR_INVALID, "%s: null group array", name);
+    if (!q || !out)
+        return fail(AROPS_ERR_INVALID, "%s: null pointer", name);
+    if (q == out)
+        return fail(AROPS_ERR_INVALID, "%s: q and out are one buffer", name);
+    st = check_workspace(name, workspace, workspace_bytes,
+                         attention_workspace_bytes(tokens, n_q_heads, cache->head_dim));
+    if (st != AROPS_OK)
+        return st;
+    AttentionParams p = {};
+    p.q = q;
+    p.out = out;
+    p.k_pages = cache->k_pages;
+    p.v_pages = cache->v_pages;
+    p.q_start = groups ? nullptr : batch->q_start;
+    p.kv_lens = batch->kv_lens;
+    p.block_table = batch->block_table;
+    if (groups) {
+        p.group_start = groups->group_start;
+        p.prefix_lens = groups->prefix_lens;
+        p.prefix_table = groups->prefix_table;
+        p.n_groups = groups->n_groups;
+        p.max_prefix_pages = groups->max_prefix_pages;
+    }
+    p.slopes = opt->slopes;
+    p.bidir_lens = opt->bidir_lens;
+    p.q_stride = q_stride;
+    p.tokens = tokens;
+    p.map = make_page_map(*cache);
+    p.n_seqs = batch->n_seqs;
+    p.max_pages = batch->max_pages;
+    p.hq = n_q_heads;
+    p.hk = cache->n_kv_heads;
+    p.head_dim = cache->head_dim;
+    p.window = opt->window;
+    p.scale = opt->scale;
+    p.softcap = opt->softcap;
+    cudaError_t err = device_error_word(&p.err);
+    if (err != cudaSuccess)
+        return from_cuda(err, name);
+    return from_cuda(launch_attention(p, cache->dtype, workspace,
+                                      static_cast<cudaStream_t>(stream)),
+                     name);
+}
+
+}  // namespace
+
+extern "C" {
+
+AROPS_API arops_status arops_mrope_paged_append(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, void* q_out, int64_t q_out_stride, const arops_paged_cache* cache,
+    const arops_paged_batch* batch, const void* gamma_q, const void* gamma_k, float eps,
+    const int32_t* pos, int64_t tokens, int32_t n_q_heads, const int32_t* sections, float theta,
+    void* stream)
+{
+    const char* name = "arops_mrope_paged_append";
+    arops_status st = check_cache(name, cache, 512);
+    if (st != AROPS_OK)
+        return st;
+    st = check_batch(name, batch, cache, tokens, true);
+    if (st != AROPS_OK)
+        return st;
+    const int32_t d = cache->head_dim, hk = cache->n_kv_heads;
+    if (n_q_heads < 0)
+        return fail(AROPS_ERR_INVALID, "%s: negative size", name);
+    if (d % 2 != 0)
+        return fail(AROPS_ERR_INVALID, "%s: head_dim must be even (got %d)", name, (int)d);
+    if (!sections)
+        return fail(AROPS_ERR_INVALID, "%s: sections is null", name);
+    if (sections[0] < 0 || sections[1] < 0 || sections[2] < 0 ||
+        (int64_t)sections[0] + sections[1] + sections[2] != d / 2)
+        return fail(AROPS_ERR_INVALID, "%s: sections [%d,%d,%d] must be >= 0 and sum to %d", name,
+                    (int)sections[0], (int)sections[1], (int)sections[2], (int)d / 2);
+    if (!(theta > 0.0f) || isinf(theta))
+        return fail(AROPS_ERR_INVALID, "%s: theta must be finite and > 0", name);
+    if ((gamma_q || gamma_k) && (!(eps >= 0.0f) || isinf(eps)))
+        return fail(AROPS_ERR_INVALID, "%s: eps must be finite and >= 0", name);
+    if ((st = check_stride(name, "q", q_stride, n_q_heads, d)) != AROPS_OK ||
+        (st = check_stride(name, "q_out", q_out_stride, n_q_heads, d)) != AROPS_OK ||
+        (st = check_stride(name, "k", k_stride, hk, d)) != AROPS_OK ||
+        (st = check_stride(name, "v", v_stride, hk, d)) != AROPS_OK)
+        return st;
+    if (tokens == 0 || batch->n_seqs == 0 || (n_q_heads == 0 && hk == 0))
+        return ok();
+    if (!pos || (n_q_heads > 0 && (!q || !q_out)) || (hk > 0 && (!k || !v)))
+        return fail(AROPS_ERR_INVALID, "%s: null pointer", name);
+    if (n_q_heads > 0 && q == q_out && q_stride != q_out_stride)
+        return fail(AROPS_ERR_INVALID, "%s: q_out is q with another stride", name);
+    PagedAppendArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_pages = cache->k_pages;
+    a.v_pages = cache->v_pages;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.q_start = batch->q_start;
+    a.kv_lens = batch->kv_lens;
+    a.block_table = batch->block_table;
+    a.pos = pos;
+    a.gamma_q = gamma_q;
+    a.gamma_k = gamma_k;
+    a.tokens = tokens;
+    a.map = make_page_map(*cache);
+    a.n_seqs = batch->n_seqs;
+    a.max_pages = batch->max_pages;
+    a.hq = n_q_heads;
+    a.hk = hk;
+    a.head_dim = d;
+    for (int i = 0; i < 3; ++i)
+        a.sections[i] = sections[i];
+    a.theta = theta;
+    a.eps = eps;
+    return from_cuda(launch_paged_append(a, cache->dtype, static_cast<cudaStream_t>(stream)),
+                     name);
+}
+
+AROPS_API arops_status arops_attention_workspace(int64_t tokens, int32_t n_q_heads,
+                                                 int32_t head_dim, size_t* bytes)
+{
+    const char* name = "arops_attention_workspace";
+    if (!bytes)
+        return fail(AROPS_ERR_INVALID, "%s: bytes is null", name);
+    if (tokens < 0 || n_q_heads < 1 || head_dim < 1)
+        return fail(AROPS_ERR_INVALID, "%s: bad shape tokens=%lld n_q_heads=%d head_dim=%d", name,
+                    (long long)tokens, (int)n_q_heads, (int)head_dim);
+    if (tokens > INT32_MAX || n_q_heads > 65535 || head_dim > 256)
+        return fail(AROPS_ERR_UNSUPPORTED,
+                    "%s: supported tokens < 2^31, n_q_heads <= 65535, head_dim <= 256", name);
+    *bytes = attention_workspace_bytes(tokens, n_q_heads, head_dim);
+    return ok();
+}
+
+AROPS_API arops_status arops_attention_prepare(void* workspace, size_t workspace_bytes,
+                                               void* stream)
+{
+    const char* name = "arops_attention_prepare";
+    const arops_status st =
+        check_workspace(name, workspace, workspace_bytes, attention_counter_bytes());
+    if (st != AROPS_OK)
+        return st;
+    return from_cuda(cudaMemsetAsync(workspace, 0, attention_counter_bytes(),
+                                     static_cast<cudaStream_t>(stream)),
+                     name);
+}
+
+AROPS_API arops_status arops_paged_attention(const void* q, int64_t q_stride, void* out,
+                                             const arops_paged_cache* cache,
+                                             const arops_paged_batch* batch,
+                                             const arops_attention_options* options,
+                                             int64_t tokens, int32_t n_q_heads, void* workspace,
+                                             size_t workspace_bytes, void* stream)
+{
+    return attention_entry("arops_paged_attention", q, q_stride, out, cache, batch, nullptr,
+                           options, tokens, n_q_heads, workspace, workspace_bytes, stream);
+}
+
+AROPS_API arops_status arops_shared_prefix_attention(
+    const void* q, int64_t q_stride, void* out, const arops_paged_cache* cache,
+    const arops_paged_batch* batch, const arops_prefix_groups* groups,
+    const arops_attention_options* options, int32_t n_q_heads, void* workspace,
+    size_t workspace_bytes, void* stream)
+{
+    const char* name = "arops_shared_prefix_attention";
+    if (!groups || !batch)
+        return fail(AROPS_ERR_INVALID, "%s: %s is null", name, groups ? "batch" : "groups");
+    return attention_entry(name, q, q_stride, out, cache, batch, groups, options, batch->n_seqs,
+                           n_q_heads, workspace, workspace_bytes, stream);
 }
 
 AROPS_API arops_status arops_swiglu(const void* gate, const void* up, void* out, int64_t rows,

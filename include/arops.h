@@ -205,12 +205,12 @@ typedef struct {
  * captured call follows their contents.  Tokens at and behind q_start[n_seqs]
  * belong to no sequence (a padded batch): nothing of theirs is written.
  * Block-table entries behind a sequence's last page are never looked at.
- * Whatever the arrays hold, nothing out of range is read or written: tokens
- * that no pair 0 <= q_start[s] <= q_start[s+1] <= tokens covers belong to no
- * sequence; a length above max_pages * page_size counts as that, and a page
- * outside the pool is not written, and read as zeros, both with
- * AROPS_DEVICE_ERR_BAD_INDEX set in the device error word.  q_start that is
- * not non-decreasing gives unspecified results within those bounds.
+ * Whatever the arrays hold, nothing out of range is read or written, and a
+ * malformed entry sets AROPS_DEVICE_ERR_BAD_INDEX in the device error word: a
+ * length above max_pages * page_size counts as that; a page outside the pool is
+ * not written, and read as zeros; attention leaves out a sequence whose pair is
+ * not 0 <= q_start[s] <= q_start[s+1] <= tokens, and the append a token that no
+ * such pair covers (without setting the bit, as it does a padding token).
  */
 typedef struct {
     const int32_t* q_start;     /* [n_seqs + 1], non-decreasing from 0 */
@@ -275,7 +275,8 @@ typedef struct {
  * n_kv_heads).  A token that sees no key gets zeros.
  *   q   [tokens, n_q_heads, head_dim], q_stride elements a token (heads dense)
  *   out [tokens, n_q_heads, head_dim] dense; not q and not part of the cache
- *   head_dim <= 256 (bf16) or 128 (fp32); n_seqs, n_q_heads <= 65535.
+ *   head_dim <= 256 (bf16) or 128 (fp32); n_seqs, n_q_heads <= 65535;
+ *   tokens * n_q_heads / n_kv_heads < 2^31.
  * Scores, softmax statistics and sums are fp32.  In bf16 the weights of the
  * second product are rounded to bf16, as q, k and v are; in fp32 both products
  * run on the tensor cores with every operand split into two tf32 parts (about
@@ -311,6 +312,8 @@ AROPS_API arops_status arops_paged_attention(const void* q, int64_t q_stride, vo
  * group_start[g] .. group_start[g+1] - 1, their first prefix_lens[g] positions
  * lie in the pages of prefix_table's row g, once for all of them.  Sequences
  * at and behind group_start[n_groups] belong to no group: they are left out.
+ * Starts that are not non-decreasing within [0, n_seqs] set
+ * AROPS_DEVICE_ERR_BAD_INDEX, and the call writes nothing.
  */
 typedef struct {
     const int32_t* group_start;  /* [n_groups + 1], non-decreasing from 0 */

@@ -366,6 +366,9 @@ arops_status attention_entry(const char* name, const void* q, int64_t q_stride, 
     if (n_q_heads < 1 || cache->n_kv_heads < 1 || n_q_heads % cache->n_kv_heads != 0)
         return fail(AROPS_ERR_INVALID, "%s: n_q_heads %d is not a multiple of n_kv_heads %d", name,
                     (int)n_q_heads, (int)cache->n_kv_heads);
+    if (tokens * (n_q_heads / cache->n_kv_heads) > INT32_MAX)
+        return fail(AROPS_ERR_UNSUPPORTED,
+                    "%s: tokens * n_q_heads / n_kv_heads must be < 2^31", name);
     if (!opt)
         return fail(AROPS_ERR_INVALID, "%s: options is null", name);
     if (!isfinite(opt->scale) || !isfinite(opt->softcap) || opt->softcap < 0.0f ||

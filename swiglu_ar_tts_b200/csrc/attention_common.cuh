@@ -60,4 +60,53 @@ __device__ __forceinline__ float map_score(float s, const ScoreMap& m, float slo
     }
 }
 
+// Units of UNIT keys that [lo, hi) takes.
+template <int UNIT>
+__device__ __forceinline__ int32_t units_between(int32_t lo, int32_t hi)
+{
+    return hi > lo ? (int32_t)(((uint32_t)(hi - lo) + UNIT - 1) / UNIT) : 0;
+}
+
+// A sequence of a ragged batch: its first token, tokens, length.
+struct Ragged {
+    int32_t t0, ntok, len, bidir;
+};
+
+__device__ __forceinline__ Ragged load_ragged(const AttentionParams& p, int32_t s, bool& bad)
+{
+    Ragged r;
+    const int64_t a = __ldg(p.q_start + s), b = __ldg(p.q_start + s + 1);
+    const bool ok = a >= 0 && b >= a && b <= p.tokens;
+    bad = bad || !ok;
+    r.t0 = ok ? (int32_t)a : 0;
+    r.ntok = ok ? (int32_t)(b - a) : 0;
+    r.len = clamp_length(__ldg(p.kv_lens + s), p.max_pages * p.map.page_size, bad);
+    r.bidir = p.bidir_lens ? __ldg(p.bidir_lens + s) : 0;
+    return r;
+}
+
+// Keys that some of rows [row0, row0 + n) sees; rows run over the tokens, g a
+// token.  The first row's keys begin first and the last row's end last.  lo is
+// rounded down to a unit.
+template <int UNIT>
+__device__ __forceinline__ void ragged_range(const AttentionParams& p, const Ragged& r, int32_t g,
+                                             uint32_t row0, uint32_t n, int32_t& lo, int32_t& hi)
+{
+    const int32_t first = (int32_t)(row0 / (uint32_t)g);
+    const int32_t last = min(r.ntok - 1, (int32_t)((row0 + n - 1) / (uint32_t)g));
+    int32_t x;
+    visible_keys(r.len - r.ntok + first, r.len, r.bidir, p.window, lo, x);
+    visible_keys(r.len - r.ntok + last, r.len, r.bidir, p.window, x, hi);
+    lo &= ~(UNIT - 1);
+}
+
+// The tile kernel (attention_tiles.cu).  With prefix_o it takes the prefixes of
+// a shared batch and leaves O (unnormalised, [tokens, hq, padded head_dim]) and
+// (m, l) of every (sequence, head) there; otherwise it writes p.out.
+bool tiles_can_run(const AttentionParams& p, arops_dtype dtype);
+size_t tile_part_bytes(int dp);
+cudaError_t launch_attention_tiles(const AttentionParams& p, int32_t* counters, float* parts,
+                                   float* prefix_o, float* prefix_ml, int sm_count,
+                                   cudaStream_t stream);
+
 }  // namespace arops

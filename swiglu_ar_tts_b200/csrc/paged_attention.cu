@@ -60,6 +60,10 @@ struct RowPlan {
     int32_t tiles_a_seq;   // shared prefixes: tiles of a sequence's heads (g > 16)
     int32_t min_units;     // of a CTA's share
     bool vec_q, vec_out;   // 16-byte q rows, 8/16-byte output groups
+    // Shared prefixes whose keys the tile kernel has already taken: O and (m, l)
+    // of every (sequence, head).  Null: this kernel takes them.
+    const float* prefix_o;
+    const float* prefix_ml;
 };
 
 // ---------------------------------------------------------------------------
@@ -168,43 +172,9 @@ struct TileKeys {
     int32_t units;   // >= 1
 };
 
-__device__ __forceinline__ int32_t units_between(int32_t lo, int32_t hi)
+__device__ __forceinline__ int32_t ragged_tiles(const Ragged& r, int32_t g)
 {
-    return hi > lo ? (int32_t)(((int64_t)hi - lo + kUnit - 1) / kUnit) : 0;
-}
-
-// -- ragged batches ----------------------------------------------------------
-struct Ragged {
-    int32_t t0, ntok, len, bidir;
-};
-
-__device__ __forceinline__ Ragged load_ragged(const AttentionParams& p, int32_t s, bool& bad)
-{
-    Ragged r;
-    const int64_t a = __ldg(p.q_start + s), b = __ldg(p.q_start + s + 1);
-    const bool ok = a >= 0 && b >= a && b <= p.tokens;
-    bad = bad || !ok;
-    r.t0 = ok ? (int32_t)a : 0;
-    r.ntok = ok ? (int32_t)(b - a) : 0;
-    r.len = clamp_length(__ldg(p.kv_lens + s), p.max_pages * p.map.page_size, bad);
-    r.bidir = p.bidir_lens ? __ldg(p.bidir_lens + s) : 0;
-    return r;
-}
-
-__device__ __forceinline__ void ragged_range(const AttentionParams& p, const Ragged& r, int32_t g,
-                                             int32_t sub, int32_t& lo, int32_t& hi)
-{
-    const int32_t first = (int32_t)((int64_t)sub * kRows / g);
-    const int32_t last = (int32_t)min((int64_t)r.ntok - 1, ((int64_t)sub * kRows + kRows - 1) / g);
-    int32_t x;
-    visible_keys(r.len - r.ntok + first, r.len, r.bidir, p.window, lo, x);
-    visible_keys(r.len - r.ntok + last, r.len, r.bidir, p.window, x, hi);
-    lo &= ~(kUnit - 1);
-}
-
-__device__ __forceinline__ int64_t ragged_tiles(const Ragged& r, int32_t g)
-{
-    return ((int64_t)r.ntok * g + kRows - 1) / kRows;
+    return (int32_t)(((uint32_t)r.ntok * g + kRows - 1) / kRows);
 }
 
 // -- shared prefixes ---------------------------------------------------------
@@ -266,7 +236,7 @@ __device__ __forceinline__ int64_t member_units(const AttentionParams& p, const 
     if (m.group < 0)
         return 0;
     const int32_t own = own_length(p, s, bad);
-    int64_t n = units_between(own_first(p, m.prefix, own), own);
+    int64_t n = units_between<kUnit>(own_first(p, m.prefix, own), own);
     if (m.index % plan.seqs_a_tile == 0) {
         int32_t lo = prefix_first(p, m.prefix, own);
         int64_t rest = 0;
@@ -274,13 +244,13 @@ __device__ __forceinline__ int64_t member_units(const AttentionParams& p, const 
         if (p.window > 0)
             for (int32_t i = 1; i < members; ++i)
                 lo = min(lo, prefix_first(p, m.prefix, own_length(p, s + i, bad)));
-        rest = units_between(lo, m.prefix);
+        rest = plan.prefix_o ? 0 : units_between<kUnit>(lo, m.prefix);
         // a tile without any key still has a unit: it writes zeros
         if (rest == 0 && n == 0) {
             bool any = false;
             for (int32_t i = 1; i < members && !any; ++i) {
                 const int32_t l = own_length(p, s + i, bad);
-                any = units_between(own_first(p, m.prefix, l), l) > 0;
+                any = units_between<kUnit>(own_first(p, m.prefix, l), l) > 0;
             }
             rest = any ? 0 : 1;
         }
@@ -299,12 +269,12 @@ __device__ __forceinline__ int64_t sequence_units(const AttentionParams& p, cons
         return member_units(p, plan, s, m, bad);
     } else {
         const Ragged r = load_ragged(p, s, bad);
-        const int64_t tiles = ragged_tiles(r, plan.g);
+        const int32_t tiles = ragged_tiles(r, plan.g);
         int64_t n = 0;
-        for (int64_t i = 0; i < tiles; ++i) {
+        for (int32_t i = 0; i < tiles; ++i) {
             int32_t lo, hi;
-            ragged_range(p, r, plan.g, (int32_t)i, lo, hi);
-            n += max(1, units_between(lo, hi));
+            ragged_range<kUnit>(p, r, plan.g, i * kRows, kRows, lo, hi);
+            n += max(1, units_between<kUnit>(lo, hi));
         }
         return n;
     }
@@ -330,7 +300,7 @@ __device__ __forceinline__ bool load_tile(const AttentionParams& p, const RowPla
         k.own_len = lane < members ? own_length(p, c.seq + lane, bad) : 0;
         k.own_lo = own_first(p, m.prefix, k.own_len);
         int32_t lo = lane < members ? prefix_first(p, m.prefix, k.own_len) : INT_MAX;
-        int32_t n = lane < members ? units_between(k.own_lo, k.own_len) : 0;
+        int32_t n = lane < members ? units_between<kUnit>(k.own_lo, k.own_len) : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
@@ -343,7 +313,7 @@ __device__ __forceinline__ bool load_tile(const AttentionParams& p, const RowPla
         k.own_end = n;
         k.lo = lo;
         k.hi = m.prefix;
-        k.prefix_units = units_between(lo, m.prefix);
+        k.prefix_units = plan.prefix_o ? 0 : units_between<kUnit>(lo, m.prefix);
         k.units = max(1, k.prefix_units + __shfl_sync(0xFFFFFFFFu, n, 31));
         return true;
     } else {
@@ -356,8 +326,8 @@ __device__ __forceinline__ bool load_tile(const AttentionParams& p, const RowPla
         k.bidir = r.bidir;
         k.group = -1;
         k.own_len = k.own_lo = k.own_end = 0;
-        ragged_range(p, r, plan.g, c.sub, k.lo, k.hi);
-        k.prefix_units = max(1, units_between(k.lo, k.hi));
+        ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, k.lo, k.hi);
+        k.prefix_units = max(1, units_between<kUnit>(k.lo, k.hi));
         k.units = k.prefix_units;
         return true;
     }
@@ -529,6 +499,35 @@ __device__ __forceinline__ void store_group(__nv_bfloat16* dst, const float* f, 
     }
 }
 
+// Four values of a row: the prefix's part joined, divided by l, stored.  A row
+// that sees no key has l == 0 and gets zeros; one that met a NaN keeps it.
+template <typename T, int DP, bool SHARED>
+__device__ __forceinline__ void store_result(const AttentionParams& p, const RowPlan& plan,
+                                             const RowOf& r, int e, float* sum, float m, float l)
+{
+    const int64_t row = (int64_t)r.token * p.hq + r.head;
+    if (SHARED && plan.prefix_o) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(plan.prefix_ml) + row);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(plan.prefix_o + row * DP + e));
+        if (ml.x != -INFINITY) {
+            const float mm = fmaxf(m, ml.x);
+            const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mm);
+            const float fp = exp2_fast(ml.x - mm);
+            l = l * f + ml.y * fp;
+            sum[0] = sum[0] * f + o.x * fp;
+            sum[1] = sum[1] * f + o.y * fp;
+            sum[2] = sum[2] * f + o.z * fp;
+            sum[3] = sum[3] * f + o.w * fp;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        sum[x] = l == 0.0f ? 0.0f : sum[x] * inv;
+    store_group<T>(static_cast<T*>(p.out) + row * p.head_dim + e, sum, min(4, p.head_dim - e),
+                   plan.vec_out);
+}
+
 template <typename T, int DP, bool VEC, bool FULL, bool SHARED>
 __global__ void __launch_bounds__(kRowThreads, RowTraits<T, DP>::kCtas)
 attention_rows_kernel(const __grid_constant__ AttentionParams p,
@@ -538,7 +537,6 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t warp_sums[kRowWarps];
     __shared__ Cursor found;
-    __shared__ int32_t found_first;  // units before the pair's cursor.unit
     __shared__ float row_m[kRowWarps][kRows], row_l[kRowWarps][kRows];
     __shared__ RowOf row_at[kRows];
     __shared__ int last_flag;
@@ -636,8 +634,8 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                 const Ragged r = load_ragged(p, s, ignore);
                 for (;; ++c.sub) {
                     int32_t lo, hi;
-                    ragged_range(p, r, plan.g, c.sub, lo, hi);
-                    tile_units = max(1, units_between(lo, hi));
+                    ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, lo, hi);
+                    tile_units = max(1, units_between<kUnit>(lo, hi));
                     if (begin < (before + tile_units) * p.hk)
                         break;
                     before += tile_units;
@@ -949,14 +947,7 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
             if (whole) {
                 if (e >= p.head_dim)
                     continue;
-                // (a row that saw a NaN or an infinity keeps it: l is not 0 then)
-                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    sum[x] = ll == 0.0f ? 0.0f : sum[x] * inv;
-                store_group<T>(static_cast<T*>(p.out) +
-                                   ((int64_t)r.token * p.hq + r.head) * p.head_dim + e,
-                               sum, min(4, p.head_dim - e), plan.vec_out);
+                store_result<T, DP, SHARED>(p, plan, r, e, sum, mm, ll);
             } else {
                 *reinterpret_cast<float4*>(part + row * DP + e) =
                     make_float4(sum[0], sum[1], sum[2], sum[3]);
@@ -1022,13 +1013,7 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                         sum[2] += v.z * f;
                         sum[3] += v.w * f;
                     }
-                    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        sum[x] = ll == 0.0f ? 0.0f : sum[x] * inv;
-                    store_group<T>(static_cast<T*>(p.out) +
-                                       ((int64_t)r.token * p.hq + r.head) * p.head_dim + e,
-                                   sum, min(4, p.head_dim - e), plan.vec_out);
+                    store_result<T, DP, SHARED>(p, plan, r, e, sum, mm, ll);
                 }
             }
         }
@@ -1101,19 +1086,30 @@ size_t attention_counter_bytes()
     return kCounterBytes;
 }
 
-size_t attention_workspace_bytes(int64_t, int, int head_dim)
+// Rows a sequence (or group) from which the tile kernel takes a call: below,
+// most of its 128-row tiles would be empty.
+constexpr int64_t kTileRowsFrom = 32;
+
+// The two kernels' partial results share a region: the second launch of a call
+// waits for the first.  The prefix's results of every (sequence, head) follow.
+size_t attention_workspace_bytes(int64_t tokens, int hq, int head_dim)
 {
-    return kCounterBytes +
-           (size_t)kMaxRowCtas * 2 * part_floats(padded_head_dim(head_dim)) * sizeof(float);
+    const int dp = padded_head_dim(head_dim);
+    size_t parts = (size_t)kMaxRowCtas * 2 * part_floats(dp) * sizeof(float);
+    if (dp > 128 || tokens * hq < kTileRowsFrom)
+        return kCounterBytes + parts;
+    return kCounterBytes + std::max(parts, tile_part_bytes(dp)) +
+           (size_t)tokens * hq * (dp + 2) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* workspace,
                              cudaStream_t stream)
 {
     DeviceInfo di;
-    const cudaError_t err = current_device_info(&di);
+    cudaError_t err = current_device_info(&di);
     if (err != cudaSuccess)
         return err;
+    const int dp = padded_head_dim(p.head_dim);
     RowPlan plan = {};
     plan.score = make_score_map(p);
     plan.counters = static_cast<int32_t*>(workspace);
@@ -1122,6 +1118,28 @@ cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* 
     plan.seqs_a_tile = std::max(1, kRows / plan.g);
     plan.tiles_a_seq = (int32_t)ceil_div(plan.g, kRows);
     plan.min_units = 1;
+
+    // Many rows a key go to the tile kernel: all of a ragged batch, or the
+    // prefixes of a shared one (a window cuts prefixes row by row: the row
+    // kernel leaves out what nobody sees).
+    const int64_t entities = p.group_start ? p.n_groups : p.n_seqs;
+    if (p.tokens * plan.g >= kTileRowsFrom * entities && tiles_can_run(p, dtype) &&
+        !(p.group_start && p.window > 0)) {
+        float* prefix_o = nullptr;
+        float* prefix_ml = nullptr;
+        if (p.group_start) {
+            const size_t parts = std::max((size_t)kMaxRowCtas * 2 * part_floats(dp) * sizeof(float),
+                                          tile_part_bytes(dp));
+            prefix_o = reinterpret_cast<float*>(reinterpret_cast<char*>(plan.parts) + parts);
+            prefix_ml = prefix_o + (size_t)p.tokens * p.hq * dp;
+        }
+        err = launch_attention_tiles(p, plan.counters, plan.parts, prefix_o, prefix_ml, di.sm_count,
+                                     stream);
+        if (err != cudaSuccess || !p.group_start)
+            return err;
+        plan.prefix_o = prefix_o;
+        plan.prefix_ml = prefix_ml;
+    }
     if (dtype == AROPS_BF16)
         return launch_rows_t<__nv_bfloat16>(p, plan, di.sm_count, stream);
     return launch_rows_t<float>(p, plan, di.sm_count, stream);

@@ -60,6 +60,27 @@ __device__ __forceinline__ float map_score(float s, const ScoreMap& m, float slo
     }
 }
 
+// Rows run over an entity's tokens, n heads each: row / n is its token.
+struct RowDivide {
+    uint32_t n;
+    int32_t shift;  // log2(n), or -1
+    __device__ __forceinline__ uint32_t operator()(uint32_t row) const
+    {
+        return shift >= 0 ? row >> shift : row / n;
+    }
+};
+
+inline RowDivide make_row_divide(int32_t n)
+{
+    RowDivide d;
+    d.n = (uint32_t)n;
+    d.shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (n == (1 << s))
+            d.shift = s;
+    return d;
+}
+
 // Units of UNIT keys that [lo, hi) takes.
 template <int UNIT>
 __device__ __forceinline__ int32_t units_between(int32_t lo, int32_t hi)
@@ -89,11 +110,12 @@ __device__ __forceinline__ Ragged load_ragged(const AttentionParams& p, int32_t 
 // token.  The first row's keys begin first and the last row's end last.  lo is
 // rounded down to a unit.
 template <int UNIT>
-__device__ __forceinline__ void ragged_range(const AttentionParams& p, const Ragged& r, int32_t g,
-                                             uint32_t row0, uint32_t n, int32_t& lo, int32_t& hi)
+__device__ __forceinline__ void ragged_range(const AttentionParams& p, const Ragged& r,
+                                             const RowDivide& g, uint32_t row0,
+                                             uint32_t n, int32_t& lo, int32_t& hi)
 {
-    const int32_t first = (int32_t)(row0 / (uint32_t)g);
-    const int32_t last = min(r.ntok - 1, (int32_t)((row0 + n - 1) / (uint32_t)g));
+    const int32_t first = (int32_t)g(row0);
+    const int32_t last = min(r.ntok - 1, (int32_t)g(row0 + n - 1));
     int32_t x;
     visible_keys(r.len - r.ntok + first, r.len, r.bidir, p.window, lo, x);
     visible_keys(r.len - r.ntok + last, r.len, r.bidir, p.window, x, hi);

@@ -35,6 +35,9 @@ constexpr int kTileRows = 2 * kSubRows;
 constexpr int kTileUnit = 128;  // keys
 constexpr int kTileThreads = 384;
 constexpr int kTileWarps = kTileThreads / 32;
+// Keys whose weights are handed to the products first, the rest follow: the
+// products of the first run under the exponentials of the rest.
+constexpr int kFirstKeys = 96;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
 
@@ -51,8 +54,9 @@ struct TileTraits {
     static constexpr int kHalves = DP / 64;              // 128-byte column blocks
     static constexpr int kSlot = kTileUnit * DP * 2;     // keys or values of a unit
     static constexpr int kQ = kSubRows * DP * 2;         // of a sub-tile
-    static constexpr int kSlots = DP == 128 ? 5 : 8;     // 160 / 128 KB
-    static constexpr int kSmem = 2 * kQ + kSlots * kSlot + 1024;  // + alignment
+    static constexpr int kSlots = DP == 128 ? 4 : 8;     // 128 KB
+    static constexpr int kStage = kSubRows * 128;        // results of a sub-tile, 64 columns
+    static constexpr int kSmem = 2 * kQ + kSlots * kSlot + 2 * kStage + 1024;  // + alignment
     static constexpr uint32_t kS = 0, kO = 2 * kTileUnit;  // columns: S_w at kS + 128 w
 };
 
@@ -62,7 +66,7 @@ struct TilePlan {
     float* parts;
     float* prefix_o;    // shared prefixes: results go here, not to out
     float* prefix_ml;
-    int32_t g;
+    RowDivide g;        // query heads a key head
     int32_t box;        // keys of one tensor-map copy
 };
 
@@ -102,14 +106,14 @@ __device__ __forceinline__ Ragged load_entity(const AttentionParams& p, int32_t 
         return load_ragged(p, s, bad);
 }
 
-__device__ __forceinline__ int32_t entity_tiles(const Ragged& r, int32_t g)
+__device__ __forceinline__ int32_t entity_tiles(const Ragged& r, const RowDivide& g)
 {
-    return (int32_t)(((uint32_t)r.ntok * g + kTileRows - 1) / kTileRows);
+    return (int32_t)(((uint32_t)r.ntok * g.n + kTileRows - 1) / kTileRows);
 }
 
 template <bool SHARED>
-__device__ __forceinline__ int32_t tile_units(const AttentionParams& p, const Ragged& r, int32_t g,
-                                              int32_t sub)
+__device__ __forceinline__ int32_t tile_units(const AttentionParams& p, const Ragged& r,
+                                              const RowDivide& g, int32_t sub)
 {
     if constexpr (SHARED) {
         return max(1, units_between<kTileUnit>(0, r.len));
@@ -122,11 +126,12 @@ __device__ __forceinline__ int32_t tile_units(const AttentionParams& p, const Ra
 
 // False: no tile `c.sub` in the entity at the cursor.
 template <bool SHARED>
-__device__ __forceinline__ bool load_span(const AttentionParams& p, int32_t g, const TileCursor& c,
-                                          TileSpan& t)
+__device__ __forceinline__ bool load_span(const AttentionParams& p, const TilePlan& plan,
+                                          const TileCursor& c, TileSpan& t)
 {
     bool bad = false;
     const Ragged r = load_entity<SHARED>(p, c.seq, bad);
+    const RowDivide g = plan.g;
     if (c.sub >= entity_tiles(r, g))
         return false;
     t.tok0 = r.t0;
@@ -135,7 +140,7 @@ __device__ __forceinline__ bool load_span(const AttentionParams& p, int32_t g, c
     t.bidir = r.bidir;
     t.table = SHARED ? p.prefix_table + (int64_t)c.seq * p.max_prefix_pages
                      : p.block_table + (int64_t)c.seq * p.max_pages;
-    const uint32_t rows = (uint32_t)r.ntok * g;
+    const uint32_t rows = (uint32_t)r.ntok * g.n;
     int32_t lo[2], hi[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -161,30 +166,53 @@ __device__ __forceinline__ bool load_span(const AttentionParams& p, int32_t g, c
     return true;
 }
 
-// The first pair at or behind the cursor; false behind the last entity.
-template <bool SHARED>
-__device__ __forceinline__ bool seek(const AttentionParams& p, int32_t g, TileCursor& c,
-                                     TileSpan& t)
-{
-    const int32_t entities = SHARED ? p.n_groups : p.n_seqs;
-    while (c.seq < entities) {
-        if (load_span<SHARED>(p, g, c, t))
-            return true;
-        ++c.seq;
-        c.sub = 0;
-    }
-    return false;
-}
+// A pair's place on the line: kPairCost positions that stand for its fixed cost
+// (queries in, results out), then its units.
+constexpr int kPairCost = 2;
 
-// On along the line, past the pair at the cursor.
-__device__ __forceinline__ void next_pair(TileCursor& c, int32_t hk)
-{
-    c.unit = 0;
-    if (++c.kvh == hk) {
-        c.kvh = 0;
-        ++c.sub;
+// A CTA's way along its share [begin, end) of the line.
+struct TileWalk {
+    TileCursor c;       // the pair to look at next
+    int64_t at;         // place of its unit 0
+    int64_t begin, end;
+
+    // c.unit: units of c's pair before `begin` (negative inside its fixed cost)
+    __device__ TileWalk(const TileCursor& from, int64_t b, int64_t e)
+        : c(from), at(b - from.unit), begin(b), end(e)
+    {
     }
-}
+
+    // The next pair with units [u0, u1) in the share, the cursor left on it;
+    // false at the end.
+    template <bool SHARED>
+    __device__ __forceinline__ bool next(const AttentionParams& p, const TilePlan& plan,
+                                         TileSpan& t, int32_t& u0, int32_t& u1)
+    {
+        const int32_t entities = SHARED ? p.n_groups : p.n_seqs;
+        while (at < end && c.seq < entities) {
+            if (!load_span<SHARED>(p, plan, c, t)) {
+                ++c.seq;
+                c.sub = 0;
+                continue;
+            }
+            u0 = (int32_t)max(begin - at, (int64_t)0);
+            u1 = (int32_t)min(end - at, (int64_t)t.units);
+            pair = c;
+            place = at;
+            at += t.units + kPairCost;
+            if (++c.kvh == p.hk) {
+                c.kvh = 0;
+                ++c.sub;
+            }
+            if (u0 < u1)
+                return true;
+        }
+        return false;
+    }
+
+    TileCursor pair;  // of the last next()
+    int64_t place;    // of its unit 0
+};
 
 // The CTA's barriers and flags in shared memory.
 template <int DP>
@@ -194,13 +222,14 @@ struct TileShared {
     uint64_t tail;      // a copy of values that reaches past the sequence's end
     uint64_t q_ready[2];
     uint64_t s_full[2];
-    uint64_t p_ready[2];
+    uint64_t p_ready[2][2];
     uint64_t o_done[2];
     uint64_t drain;
     uint32_t tmem;
     int stop;           // a wait ran out: everybody leaves
     int last[2];
     int64_t sums[kTileWarps];
+    int64_t found_before;  // line in front of the found entity, per key head
     TileCursor found;
 };
 
@@ -231,21 +260,19 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* st
 template <int DP, bool SHARED>
 __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                                const CUtensorMap* kmap, const CUtensorMap* vmap,
-                               unsigned char* slots, TileShared<DP>& sh, TileCursor c, int64_t left,
-                               int lane)
+                               unsigned char* slots, TileShared<DP>& sh, TileCursor c, int64_t begin,
+                               int64_t end, int lane)
 {
     using R = TileTraits<DP>;
     const int boxes = kTileUnit / plan.box;
     uint32_t n = 0;      // slots filled
     uint32_t tails = 0;  // copies waited for here
     bool ok = true;
-    while (ok && left > 0) {
-        TileSpan t;
-        if (!seek<SHARED>(p, plan.g, c, t))
-            break;
-        const int32_t u1 = (int32_t)min((int64_t)t.units, c.unit + left);
-        left -= u1 - c.unit;
-        for (int32_t u = c.unit; ok && u < u1; ++u) {
+    TileWalk walk(c, begin, end);
+    TileSpan t;
+    int32_t u0, u1;
+    while (ok && walk.next<SHARED>(p, plan, t, u0, u1)) {
+        for (int32_t u = u0; ok && u < u1; ++u) {
             const int32_t key0 = t.lo + u * kTileUnit;
             const int32_t key = key0 + lane * plan.box;
             // a copy of a page that does not exist brings zeros
@@ -278,7 +305,8 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
 #pragma unroll
                     for (int h = 0; h < R::kHalves; ++h)
                         tensor_load4(smem_addr(dst) + h * (kTileUnit * 128) + lane * plan.box * 128,
-                                     kv ? vmap : kmap, bar, h * 64, slot, c.kvh, page);
+                                     kv ? vmap : kmap, bar, h * 64, slot, walk.pair.kvh,
+                                     page);
                 }
                 if (clean) {
                     // slots behind the sequence's end may hold anything, and 0
@@ -303,7 +331,6 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                 ++n;
             }
         }
-        next_pair(c, p.hk);
     }
     if (!ok) {
         // nothing is left in flight: the copies issued last (bounded)
@@ -313,29 +340,31 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
 }
 
 // ---------------------------------------------------------------------------
-// Products (one thread).
+// Products (one warp; one thread of it issues).
 // ---------------------------------------------------------------------------
 template <int DP, bool SHARED>
 __device__ void tile_mma_role(const AttentionParams& p, const TilePlan& plan,
                               const unsigned char* q, const unsigned char* slots,
-                              TileShared<DP>& sh, TileCursor c, int64_t left)
+                              TileShared<DP>& sh, TileCursor c, int64_t begin, int64_t end)
 {
     using R = TileTraits<DP>;
     constexpr uint32_t kWordS = mma_word(kSubRows, kTileUnit, false);
     constexpr uint32_t kWordO = mma_word(kSubRows, DP, true);
     const uint32_t tmem = sh.tmem;
+    // keys and queries: K (head_dim) contiguous, one 64-value block behind the
+    // other; values: N (head_dim) contiguous, the leading offset between blocks
+    const uint32_t q_low = operand_low(smem_addr(q), 16);
+    const uint32_t k_low = operand_low(smem_addr(slots), 16);
+    const uint32_t v_low = operand_low(smem_addr(slots), kTileUnit * 128);
     uint32_t used = 0;                   // slots consumed
     uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wait_for(bar, parity, &sh.stop, p.err);
+        return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, &sh.stop, p.err));
     };
-    while (left > 0) {
-        TileSpan t;
-        if (!seek<SHARED>(p, plan.g, c, t))
-            break;
-        const int32_t u0 = c.unit;
-        const int32_t u1 = (int32_t)min((int64_t)t.units, u0 + left);
-        left -= u1 - u0;
+    TileWalk walk(c, begin, end);
+    TileSpan t;
+    int32_t u0, u1;
+    while (walk.next<SHARED>(p, plan, t, u0, u1)) {
         int32_t a[2], b[2];  // the sub-tiles' units of this share
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
@@ -357,23 +386,34 @@ __device__ void tile_mma_role(const AttentionParams& p, const TilePlan& plan,
                     return;
                 ++used;
             }
-            const uint32_t vaddr = smem_addr(slots + vs * R::kSlot);
-            const uint32_t kaddr = smem_addr(slots + ks * R::kSlot);
+            const uint32_t vb = v_low + vs * (R::kSlot >> 4);
+            const uint32_t kb = k_low + ks * (R::kSlot >> 4);
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
+                const uint32_t o = tmem + R::kO + w * DP;
+                const uint32_t s = tmem + R::kS + w * kTileUnit;
                 if (u >= a[w] && u < b[w]) {  // O_w (+)= P_w V
-                    if (!wait(&sh.p_ready[w], pn[w] & 1))
+                    if (!wait(&sh.p_ready[w][0], pn[w] & 1))
                         return;
-                    ++pn[w];
                     tc_fence_after();
-                    const uint32_t o = tmem + R::kO + w * DP;
-                    const uint32_t s = tmem + R::kS + w * kTileUnit;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kTileUnit / 16; ++k)
-                        tc_mma_ts(o, s + k * 8,
-                                  operand_desc(vaddr + k * 2048, kTileUnit * 128, 1024), kWordO,
-                                  u > a[w] || k > 0);
-                    tc_commit(smem_addr(&sh.o_done[w]));
+                        for (int k = 0; k < kFirstKeys / 16; ++k)
+                            tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO,
+                                      u > a[w] || k > 0);
+                    }
+                    __syncwarp();
+                    if (!wait(&sh.p_ready[w][1], pn[w] & 1))
+                        return;
+                    tc_fence_after();
+                    ++pn[w];
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = kFirstKeys / 16; k < kTileUnit / 16; ++k)
+                            tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO, true);
+                        tc_commit(smem_addr(&sh.o_done[w]));
+                    }
+                    __syncwarp();
                 }
                 if (u + 1 >= a[w] && u + 1 < b[w]) {  // the next S_w = Q_w K^T
                     if (u + 1 == a[w]) {
@@ -382,23 +422,25 @@ __device__ void tile_mma_role(const AttentionParams& p, const TilePlan& plan,
                         ++qn[w];
                         tc_fence_after();
                     }
-                    const uint32_t s = tmem + R::kS + w * kTileUnit;
-                    const uint32_t qaddr = smem_addr(q + w * R::kQ);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t off = (k / 4) * (kTileUnit * 128) + (k % 4) * 32;
-                        tc_mma_ss(s, operand_desc(qaddr + off, 16, 1024),
-                                  operand_desc(kaddr + off, 16, 1024), kWordS, k > 0);
+                        for (int k = 0; k < DP / 16; ++k) {
+                            const uint32_t off = ((k / 4) * (kTileUnit * 128) + (k % 4) * 32) >> 4;
+                            tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off, kb + off, kWordS, k > 0);
+                        }
+                        tc_commit(smem_addr(&sh.s_full[w]));
                     }
-                    tc_commit(smem_addr(&sh.s_full[w]));
+                    __syncwarp();
                 }
             }
-            if (u >= u0)
-                tc_commit(smem_addr(&sh.empty[vs]));
-            if (u + 1 < u1)
-                tc_commit(smem_addr(&sh.empty[ks]));
+            if (elect_one()) {
+                if (u >= u0)
+                    tc_commit(smem_addr(&sh.empty[vs]));
+                if (u + 1 < u1)
+                    tc_commit(smem_addr(&sh.empty[ks]));
+            }
+            __syncwarp();
         }
-        next_pair(c, p.hk);
     }
 }
 
@@ -410,38 +452,115 @@ __device__ __forceinline__ void sub_tile_barrier(int w)
     asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
 }
 
+// (token, head) of rows that a thread takes `step` apart.
+struct RowStep {
+    uint32_t tok, head, g, dt, dh;
+    __device__ __forceinline__ RowStep(const RowDivide& d, uint32_t row, uint32_t step) : g(d.n)
+    {
+        tok = d(row);
+        head = row - tok * g;
+        dt = d(step);
+        dh = step - dt * g;
+    }
+    __device__ __forceinline__ void next()
+    {
+        tok += dt;
+        head += dh;
+        if (head >= g) {
+            head -= g;
+            ++tok;
+        }
+    }
+};
+
 // The sub-tile's query rows into shared memory (asynchronous copies).
 template <int DP>
-__device__ __forceinline__ void load_q_rows(const AttentionParams& p, int32_t g,
+__device__ __forceinline__ void load_q_rows(const AttentionParams& p, const RowDivide& g,
                                             const TileSpan& t, const TileCursor& c, int w,
                                             unsigned char* q, int tid)
 {
     constexpr int kChunks = DP / 8;
-    const int used = p.head_dim / 8;
-    const uint32_t dst = smem_addr(q);
+    constexpr int kStep = 128 / kChunks;
+    const int chunk = tid % kChunks;
+    int row = tid / kChunks;
+    const bool used = chunk < p.head_dim / 8;
+    RowStep r(g, (uint32_t)c.sub * kTileRows + w * kSubRows + row, kStep);
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.q) +
+                                t.tok0 * p.q_stride + (int64_t)c.kvh * g.n * p.head_dim +
+                                chunk * 8;
+    const uint32_t dst = smem_addr(q) + (chunk / 8) * (kSubRows * 128);
 #pragma unroll 4
-    for (int i = 0; i < kSubRows * kChunks / 128; ++i) {
-        const int idx = i * 128 + tid;
-        const int row = idx / kChunks, chunk = idx % kChunks;
-        const uint32_t at = (uint32_t)c.sub * kTileRows + w * kSubRows + row;
-        const uint32_t tok = at / (uint32_t)g;
-        const uint32_t head = c.kvh * g + (at - tok * g);
-        const bool ok = tok < (uint32_t)t.ntok && chunk < used;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q);
-        if (ok)
-            src += (int64_t)(t.tok0 + tok) * p.q_stride + (int64_t)head * p.head_dim + chunk * 8;
-        const uint32_t d =
-            dst + (chunk / 8) * (kSubRows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src),
-                     "r"(ok ? 16u : 0u)
+    for (int i = 0; i < kSubRows / kStep; ++i) {
+        const bool ok = r.tok < (uint32_t)t.ntok && used;
+        const __nv_bfloat16* src =
+            ok ? base + (int64_t)r.tok * p.q_stride + r.head * p.head_dim
+               : static_cast<const __nv_bfloat16*>(p.q);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         dst + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)),
+                     "l"(src), "r"(ok ? 16u : 0u)
                      : "memory");
+        row += kStep;
+        r.next();
+    }
+}
+
+// 64 columns of a sub-tile's results, a row a thread, divided by l: through
+// shared memory, so that eight threads store a row's 128 bytes together.
+template <int DP, bool SHARED>
+__device__ __forceinline__ void emit_columns(const AttentionParams& p, const TilePlan& plan,
+                                             const TileSpan& t, const TileCursor& c,
+                                             const uint32_t (&o)[64], int col, float m, float l,
+                                             unsigned char* stage, int w, int tid)
+{
+    const uint32_t row0 = (uint32_t)c.sub * kTileRows + w * kSubRows;
+    if constexpr (SHARED) {
+        const RowStep r(plan.g, row0 + tid, 1);
+        if (r.tok < (uint32_t)t.ntok) {
+            const int64_t at = (int64_t)(t.tok0 + r.tok) * p.hq + c.kvh * plan.g.n + r.head;
+            float4* dst = reinterpret_cast<float4*>(plan.prefix_o + at * DP + col);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            if (col == 0)
+                *reinterpret_cast<float2*>(plan.prefix_ml + at * 2) = make_float2(m, l);
+        }
+    } else {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float y[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                y[x] = l == 0.0f ? 0.0f : __uint_as_float(o[8 * e + x]) * inv;
+            *reinterpret_cast<uint4*>(stage + tid * 128 + ((e ^ (tid & 7)) << 4)) =
+                Vec<__nv_bfloat16>::pack(y);
+        }
+        sub_tile_barrier(w);
+        const int chunk = tid & 7;
+        int row = tid >> 3;
+        RowStep r(plan.g, row0 + row, 16);
+        __nv_bfloat16* base = static_cast<__nv_bfloat16*>(p.out) +
+                              ((int64_t)t.tok0 * p.hq + c.kvh * plan.g.n) * p.head_dim + col +
+                              chunk * 8;
+        const bool used = col + chunk * 8 < p.head_dim;
+#pragma unroll
+        for (int i = 0; i < kSubRows / 16; ++i) {
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(stage + row * 128 + ((chunk ^ (row & 7)) << 4));
+            if (used && r.tok < (uint32_t)t.ntok)
+                *reinterpret_cast<uint4*>(base + ((int64_t)r.tok * p.hq + r.head) * p.head_dim) = v;
+            row += 16;
+            r.next();
+        }
+        sub_tile_barrier(w);
     }
 }
 
 template <int DP, bool FULL, bool SHARED>
 __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan, unsigned char* q,
-                                  TileShared<DP>& sh, TileCursor c, int64_t left, int64_t begin,
-                                  int64_t share, int w, int tid)
+                                  unsigned char* stage, TileShared<DP>& sh, const TileCursor& from,
+                                  int64_t begin, int64_t end, int64_t share, int w, int tid)
 {
     using R = TileTraits<DP>;
     const int lane = tid & 31;
@@ -449,55 +568,54 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
     const uint32_t s_addr = sh.tmem + lanes + R::kS + w * kTileUnit;
     const uint32_t o_addr = sh.tmem + lanes + R::kO + w * DP;
     uint32_t sn = 0, on = 0;  // S tiles seen, P V products asked for
-    int64_t at = begin;
 
-    // the first tile's queries; later ones are asked for under the last unit of
-    // the tile before
-    TileSpan t;
-    auto next_queries = [&]() {
-        if (!seek<SHARED>(p, plan.g, c, t)) {
-            left = 0;
-            return;
-        }
-        load_q_rows<DP>(p, plan.g, t, c, w, q, tid);
-    };
-    next_queries();
     // once a wait has run out a warp does nothing but keep the barriers
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         dead = !__all_sync(0xFFFFFFFFu, !dead && wait_for(bar, parity, &sh.stop, p.err));
         return !dead;
     };
+    // the first tile's queries; later ones are asked for under the last unit of
+    // the tile before
+    TileWalk walk(from, begin, end);
+    TileSpan next_t;
+    int32_t next_u0, next_u1;
+    auto next_queries = [&]() {
+        const bool more = walk.next<SHARED>(p, plan, next_t, next_u0, next_u1);
+        if (more)
+            load_q_rows<DP>(p, plan.g, next_t, walk.pair, w, q, tid);
+        return more;
+    };
+    bool more = next_queries();
 
-    while (left > 0) {
-        const int32_t u0 = c.unit;
-        const int32_t u1 = (int32_t)min((int64_t)t.units, u0 + left);
-        left -= u1 - u0;
+    while (more) {
+        const TileSpan t = next_t;
+        const TileCursor c = walk.pair;
+        const int64_t place = walk.place;
+        const int32_t u0 = next_u0, u1 = next_u1;
         const int32_t a = max(t.jlo[w], u0), b = min(t.jhi[w], u1);
 
         // this thread's row
-        const uint32_t row = (uint32_t)c.sub * kTileRows + w * kSubRows + tid;
-        const int32_t index = (int32_t)(row / (uint32_t)plan.g);
-        const int32_t head = c.kvh * plan.g + (int32_t)(row - (uint32_t)index * plan.g);
-        const bool valid = index < t.ntok;
+        const RowStep r(plan.g, (uint32_t)c.sub * kTileRows + w * kSubRows + tid, 1);
+        const bool valid = r.tok < (uint32_t)t.ntok;
         int32_t pos, lo = 0, hi = t.len;
         if constexpr (SHARED) {
             bool ignore = false;
             pos = t.len - 1;
             if (FULL && valid)
-                pos += clamp_length(__ldg(p.kv_lens + t.tok0 + index),
+                pos += clamp_length(__ldg(p.kv_lens + t.tok0 + r.tok),
                                     p.max_pages * p.map.page_size, ignore);
         } else {
-            pos = t.len - t.ntok + index;
+            pos = t.len - t.ntok + (int32_t)r.tok;
             if (valid)
                 visible_keys(pos, t.len, t.bidir, p.window, lo, hi);
             else
                 hi = INT_MAX;  // nobody reads such a row
         }
-        const float slope = FULL && p.slopes && valid ? __ldg(p.slopes + head) : 0.0f;
+        const float slope =
+            FULL && p.slopes && valid ? __ldg(p.slopes + c.kvh * plan.g.n + r.head) : 0.0f;
         const float scale = FULL ? 1.0f : plan.score.scale;
 
-        const TileSpan span = t;
         bool asked = false;  // for the next tile's queries
         if (a < b) {
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -512,20 +630,19 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                 break;
             ++sn;
             tc_fence_after();
+            if (u + 1 == b) {
+                // Q_w has been read for the last time
+                more = next_queries();
+                asked = true;
+            }
             uint32_t s[kTileUnit];
 #pragma unroll
             for (int i = 0; i < kTileUnit; i += 32)
                 tc_load32(s + i, s_addr + i);
-            if (u + 1 == b && left > 0) {
-                // Q_w has been read for the last time: the next tile's queries
-                next_pair(c, p.hk);
-                next_queries();
-                asked = true;
-            }
             tc_wait_ld();
             tc_loaded<kTileUnit>(s);
 
-            const int32_t key0 = span.lo + u * kTileUnit;
+            const int32_t key0 = t.lo + u * kTileUnit;
             if constexpr (FULL) {
 #pragma unroll
                 for (int i = 0; i < kTileUnit; ++i)
@@ -533,19 +650,27 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                                                            slope, pos, key0 + i));
             }
             if (__any_sync(0xFFFFFFFFu, key0 < lo || hi - key0 < kTileUnit)) {
-                const int32_t from = lo - key0, to = hi - key0;
+                const int32_t first = lo - key0, last = hi - key0;
 #pragma unroll
                 for (int i = 0; i < kTileUnit; ++i)
-                    s[i] = i >= from && i < to ? s[i] : __float_as_uint(-INFINITY);
+                    s[i] = i >= first && i < last ? s[i] : __float_as_uint(-INFINITY);
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[8];
 #pragma unroll
-            for (int i = 0; i < kTileUnit; i += 8)
+            for (int e = 0; e < 8; ++e)
+                mx[e] = __uint_as_float(s[e]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+            for (int i = 8; i < kTileUnit - 8; i += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
                     mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[i + e])),
-                                  __uint_as_float(s[i + 4 + e]));
-            const float mu = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                                  __uint_as_float(s[i + 8 + e]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                mx[e] = fmaxf(mx[e], __uint_as_float(s[kTileUnit - 8 + e]));
+            const float mu = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
+                             scale;
 
             // scale what there is only when a maximum has grown by 2^8
             const bool grown = mu > m + 8.0f || (m == -INFINITY && mu > -INFINITY);
@@ -559,15 +684,15 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                         break;
                     tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < DP; i += 32) {
-                        uint32_t o[32];
-                        tc_load32(o, o_addr + i);
+                    for (int i = 0; i < DP; i += 16) {
+                        uint32_t o[16];
+                        tc_load16(o, o_addr + i);
                         tc_wait_ld();
-                        tc_loaded<32>(o);
+                        tc_loaded<16>(o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc_store32(o_addr + i, o);
+                        tc_store16(o_addr + i, o);
                     }
                 }
             }
@@ -577,10 +702,10 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
             // the weights are rounded to bf16 (2^-8 of each at most), the type
             // of the values that they multiply; l keeps them in fp32
 #pragma unroll
-            for (int i = 0; i < kTileUnit; i += 64) {
-                uint32_t pk[32];
+            for (int i = 0; i < kTileUnit; i += 32) {
+                uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
+                for (int e = 0; e < 32; e += 2) {
                     float2 x = make_float2(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1]));
                     x = fma2(x, sc, bs);
                     x.x = exp2_fast(x.x);
@@ -588,80 +713,52 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                     sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
                     pk[e >> 1] = pack_bf16x2(x.x, x.y);
                 }
-                tc_store32(s_addr + i / 2, pk);
+                tc_store16(s_addr + i / 2, pk);
+                if (i + 32 == kFirstKeys || i + 32 == kTileUnit) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sh.p_ready[w][i + 32 == kTileUnit]));
+                }
             }
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_addr(&sh.p_ready[w]));
             ++on;
             const float2 all = add2(sum[0], sum[1]);
             l += all.x + all.y;
         }
-        if (!asked && left > 0) {  // no unit of this sub-tile here
+        if (!asked) {  // no unit of this sub-tile here
             asm volatile("cp.async.wait_all;" ::: "memory");
-            next_pair(c, p.hk);
-            next_queries();
+            more = next_queries();
         }
         const bool has = a < b && wait(&sh.o_done[w], (on - 1) & 1);
         tc_fence_after();
 
         // -- results -----------------------------------------------------------
-        const bool whole = u0 == 0 && u1 == span.units;
-        const int64_t pair0 = at - u0;
-        at += u1 - u0;
-        const int32_t cta0 = (int32_t)(pair0 / share);
-        const int32_t cta1 = (int32_t)((pair0 + span.units - 1) / share);
+        const bool whole = u0 == 0 && u1 == t.units;
+        const int32_t cta0 = (int32_t)(place / share);
+        const int32_t cta1 = (int32_t)((place + t.units - 1) / share);
         auto part_of = [&](int32_t x) {
             return plan.parts + ((int64_t)x * 4 + (x == cta0 ? 2 : 0) + w) * tile_part_floats(DP);
         };
-        const int64_t out_row = (int64_t)(span.tok0 + index) * p.hq + head;
-        auto store_columns = [&](const float* f, int i, float mm, float ll) {
-            if (!valid)
-                return;
-            if constexpr (SHARED) {
-                float4* dst = reinterpret_cast<float4*>(plan.prefix_o + out_row * DP + i);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                if (i == 0)
-                    *reinterpret_cast<float2*>(plan.prefix_ml + out_row * 2) = make_float2(mm, ll);
-            } else {
-                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + out_row * p.head_dim + i;
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    if (i + e >= p.head_dim)
-                        break;
-                    float y[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        y[x] = ll == 0.0f ? 0.0f : f[e + x] * inv;
-                    *reinterpret_cast<uint4*>(dst + e) = Vec<__nv_bfloat16>::pack(y);
-                }
-            }
-        };
         float* part = part_of(blockIdx.x);
-        if (u0 != 0)
-            part = plan.parts + ((int64_t)blockIdx.x * 4 + w) * tile_part_floats(DP);
 #pragma unroll
-        for (int i = 0; i < DP; i += 32) {
-            uint32_t o[32];
+        for (int i = 0; i < DP; i += 64) {
+            uint32_t o[64];
             if (has) {
                 tc_load32(o, o_addr + i);
+                tc_load32(o + 32, o_addr + i + 32);
                 tc_wait_ld();
-                tc_loaded<32>(o);
+                tc_loaded<64>(o);
             } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < 64; ++e)
                     o[e] = 0;
             }
             if (whole) {
-                store_columns(reinterpret_cast<const float*>(o), i, m, l);
+                emit_columns<DP, SHARED>(p, plan, t, c, o, i, m, l, stage, w, tid);
             } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
+                for (int e = 0; e < 64; e += 4)
                     *reinterpret_cast<uint4*>(part + ((i + e) / 4 * kSubRows + tid) * 4) =
                         make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
@@ -684,40 +781,46 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                 }
             }
             sub_tile_barrier(w);
-            if (sh.last[w]) {
+            const bool join = sh.last[w];
+            sub_tile_barrier(w);  // the flag has been read
+            if (join) {
                 float mm = -INFINITY, ll = 0.0f;
-                for (int32_t x = cta0; x <= cta1; ++x)
-                    mm = fmaxf(mm, __ldcg(part_of(x) + kSubRows * DP + tid));
                 for (int32_t x = cta0; x <= cta1; ++x) {
                     const float mx = __ldcg(part_of(x) + kSubRows * DP + tid);
+                    const float lx = __ldcg(part_of(x) + kSubRows * DP + kSubRows + tid);
+                    const float mn = fmaxf(mm, mx);
                     if (mx != -INFINITY)
-                        ll += __ldcg(part_of(x) + kSubRows * DP + kSubRows + tid) *
-                              exp2_fast(mx - mm);
+                        ll = (mm == -INFINITY ? 0.0f : ll * exp2_fast(mm - mn)) +
+                             lx * exp2_fast(mx - mn);
+                    mm = mn;
                 }
 #pragma unroll 1
-                for (int i = 0; i < DP; i += 32) {
-                    float f[32];
+                for (int i = 0; i < DP; i += 64) {
+                    uint32_t o[64];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        f[e] = 0.0f;
+                    for (int e = 0; e < 64; ++e)
+                        o[e] = 0;
                     for (int32_t x = cta0; x <= cta1; ++x) {
                         const float* src = part_of(x);
                         const float mx = __ldcg(src + kSubRows * DP + tid);
+                        uint4 v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            v[e] = __ldcg(reinterpret_cast<const uint4*>(
+                                src + ((i / 4 + e) * kSubRows + tid) * 4));
                         const float fx = mx == -INFINITY ? 0.0f : exp2_fast(mx - mm);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                                src + ((i + e) / 4 * kSubRows + tid) * 4));
-                            f[e] += v.x * fx;
-                            f[e + 1] += v.y * fx;
-                            f[e + 2] += v.z * fx;
-                            f[e + 3] += v.w * fx;
+                        for (int e = 0; e < 16; ++e) {
+                            const uint32_t y[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                o[4 * e + z] = __float_as_uint(fmaf(
+                                    __uint_as_float(y[z]), fx, __uint_as_float(o[4 * e + z])));
                         }
                     }
-                    store_columns(f, i, mm, ll);
+                    emit_columns<DP, SHARED>(p, plan, t, c, o, i, mm, ll, stage, w, tid);
                 }
             }
-            sub_tile_barrier(w);  // the flag has been read
         }
     }
 }
@@ -735,6 +838,7 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     unsigned char* q = smem;
     unsigned char* slots = smem + 2 * R::kQ;
+    unsigned char* stages = slots + R::kSlots * R::kSlot;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -747,7 +851,8 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_addr(&sh.q_ready[w]), 4);
             mbar_init(smem_addr(&sh.s_full[w]), 1);
-            mbar_init(smem_addr(&sh.p_ready[w]), 4);
+            mbar_init(smem_addr(&sh.p_ready[w][0]), 4);
+            mbar_init(smem_addr(&sh.p_ready[w][1]), 4);
             mbar_init(smem_addr(&sh.o_done[w]), 1);
         }
         sh.stop = 0;
@@ -756,22 +861,39 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     pdl_wait();
     pdl_allow_dependents();
 
-    // -- this CTA's share of the line of units --------------------------------
+    // -- this CTA's share of the line -----------------------------------------
+    // `tps` threads count an entity's tiles together
     const int32_t entities = SHARED ? p.n_groups : p.n_seqs;
     bool bad = false;
-    const int32_t per = (entities + kTileThreads - 1) / kTileThreads;
-    const int32_t e0 = (int32_t)min((int64_t)threadIdx.x * per, (int64_t)entities);
+    int32_t tps = 32;
+    while (tps > 1 && (int64_t)entities * tps > kTileThreads)
+        tps /= 2;
+    const int32_t sets = kTileThreads / tps;
+    const int32_t per = (entities + sets - 1) / sets;
+    const int32_t e0 = min((int32_t)threadIdx.x / tps * per, entities);
     const int32_t e1 = min(e0 + per, entities);
-    auto count = [&](const Ragged& r) {
+    auto count = [&](const Ragged& r, int32_t first, int32_t step) {
         const int32_t tiles = entity_tiles(r, plan.g);
         int64_t n = 0;
-        for (int32_t i = 0; i < tiles; ++i)
-            n += tile_units<SHARED>(p, r, plan.g, i);
+        for (int32_t i = first; i < tiles; i += step)
+            n += tile_units<SHARED>(p, r, plan.g, i) + kPairCost;
         return n;
     };
     int64_t mine = 0;
+    bool broken = false;  // starts of groups that do not follow one another
+    if constexpr (SHARED)
+        for (int32_t e = e0; e < e1; ++e) {
+            const int32_t a = __ldg(p.group_start + e), b = __ldg(p.group_start + e + 1);
+            broken = broken || a < 0 || b < a || b > p.n_seqs;
+        }
     for (int32_t e = e0; e < e1; ++e)
-        mine += count(load_entity<SHARED>(p, e, bad));
+        mine += count(load_entity<SHARED>(p, e, bad), threadIdx.x % tps, tps);
+    __syncwarp();
+    for (int o = 1; o < tps; o <<= 1)
+        mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    const bool leads = threadIdx.x % tps == 0;
+    if (!leads)
+        mine = 0;
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -781,8 +903,8 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     }
     if (lane == 31)
         sh.sums[warp] = upto;
-    if (__syncthreads_or(SHARED && bad)) {  // malformed groups: nothing is written
-        if (bad && blockIdx.x == 0)
+    if (__syncthreads_or(broken)) {  // nothing is written
+        if (threadIdx.x == 0 && blockIdx.x == 0)
             record_device_error(p.err, kDeviceErrBadIndexBit);
         return;
     }
@@ -800,31 +922,48 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     const int64_t begin = (int64_t)blockIdx.x * share;
     if (begin >= line)
         return;
-    const int64_t left = min(share, line - begin);
-    int64_t before = upto - mine;
-    if (begin >= before * p.hk && begin < upto * p.hk) {
-        TileCursor c;
-        c.seq = e0;
+    const int64_t end = min(begin + share, line);
+    if (leads && begin >= (upto - mine) * p.hk && begin < upto * p.hk) {
+        int64_t before = upto - mine;
+        int32_t e = e0;
         bool ignore = false;
-        Ragged r;
-        for (;; ++c.seq) {
-            r = load_entity<SHARED>(p, c.seq, ignore);
-            const int64_t n = count(r);
+        for (; e + 1 < e1; ++e) {
+            const int64_t n = count(load_entity<SHARED>(p, e, ignore), 0, 1);
             if (begin < (before + n) * p.hk)
                 break;
             before += n;
         }
-        int64_t n = 1;
-        for (c.sub = 0;; ++c.sub) {
-            n = tile_units<SHARED>(p, r, plan.g, c.sub);
-            if (begin < (before + n) * p.hk)
+        sh.found.seq = e;
+        sh.found_before = before;
+    }
+    __syncthreads();
+    if (warp == 0) {  // the tile within the entity, 32 at a time
+        bool ignore = false;
+        const Ragged r = load_entity<SHARED>(p, sh.found.seq, ignore);
+        const int32_t tiles = entity_tiles(r, plan.g);
+        int64_t before = sh.found_before;
+        for (int32_t i0 = 0; i0 < tiles; i0 += 32) {
+            const int32_t n =
+                i0 + lane < tiles ? tile_units<SHARED>(p, r, plan.g, i0 + lane) + kPairCost : 0;
+            int64_t sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o)
+                    sum += x;
+            }
+            const unsigned in = __ballot_sync(0xFFFFFFFFu, begin < (before + sum) * p.hk);
+            if (in != 0) {
+                if (lane == __ffs(in) - 1) {
+                    const int64_t rest = begin - (before + sum - n) * p.hk;
+                    sh.found.sub = i0 + lane;
+                    sh.found.kvh = (int32_t)(rest / n);
+                    sh.found.unit = (int32_t)(rest % n) - kPairCost;
+                }
                 break;
-            before += n;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
-        const int64_t rest = begin - before * p.hk;
-        c.kvh = (int32_t)(rest / n);
-        c.unit = (int32_t)(rest % n);
-        sh.found = c;
     }
     if (warp == kMmaWarp)
         tc_alloc(smem_addr(&sh.tmem));
@@ -838,20 +977,20 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int w = warp >> 2;
-        tile_softmax_role<DP, FULL, SHARED>(p, plan, q + w * R::kQ, sh, c, left, begin, share, w,
-                                            threadIdx.x & 127);
+        tile_softmax_role<DP, FULL, SHARED>(p, plan, q + w * R::kQ, stages + w * R::kStage, sh, c,
+                                            begin, end, share, w, threadIdx.x & 127);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kMmaWarp) {
-            if (lane == 0) {
-                tile_mma_role<DP, SHARED>(p, plan, q, slots, sh, c, left);
-                // every product and every arrival asked for has happened
+            tile_mma_role<DP, SHARED>(p, plan, q, slots, sh, c, begin, end);
+            // every product and every arrival asked for has happened
+            if (elect_one())
                 tc_commit(smem_addr(&sh.drain));
-                mbar_wait(smem_addr(&sh.drain), 0);
-            }
+            __syncwarp();
+            mbar_wait(smem_addr(&sh.drain), 0);
             __syncwarp();
         } else if (warp == kLoadWarp) {
-            tile_load_role<DP, SHARED>(p, plan, &kmap, &vmap, slots, sh, c, left, lane);
+            tile_load_role<DP, SHARED>(p, plan, &kmap, &vmap, slots, sh, c, begin, end, lane);
             __syncwarp();
         }
     }
@@ -971,7 +1110,7 @@ cudaError_t launch_attention_tiles(const AttentionParams& p, int32_t* counters, 
     plan.parts = parts;
     plan.prefix_o = prefix_o;
     plan.prefix_ml = prefix_ml;
-    plan.g = p.hq / p.hk;
+    plan.g = make_row_divide(p.hq / p.hk);
     plan.box = box_slots(p.map.page_size);
     CUtensorMap kmap, vmap;
     cudaError_t err = pool_map(&kmap, p.k_pages, p, plan.box);

@@ -55,7 +55,7 @@ struct RowPlan {
     ScoreMap score;
     int32_t* counters;
     float* parts;
-    int32_t g;             // query heads a key head
+    RowDivide g;           // query heads a key head
     int32_t seqs_a_tile;   // shared prefixes: sequences of a tile (g <= 16)
     int32_t tiles_a_seq;   // shared prefixes: tiles of a sequence's heads (g > 16)
     int32_t min_units;     // of a CTA's share
@@ -172,9 +172,9 @@ struct TileKeys {
     int32_t units;   // >= 1
 };
 
-__device__ __forceinline__ int32_t ragged_tiles(const Ragged& r, int32_t g)
+__device__ __forceinline__ int32_t ragged_tiles(const Ragged& r, const RowDivide& g)
 {
-    return (int32_t)(((uint32_t)r.ntok * g + kRows - 1) / kRows);
+    return (int32_t)(((uint32_t)r.ntok * g.n + kRows - 1) / kRows);
 }
 
 // -- shared prefixes ---------------------------------------------------------
@@ -467,8 +467,8 @@ __device__ __forceinline__ RowOf row_of(const TileKeys& k, const RowPlan& plan, 
 {
     RowOf r;
     const uint32_t at = (uint32_t)c.sub * kRows + row;
-    r.index = (int32_t)(at / (uint32_t)plan.g);
-    r.head = c.kvh * plan.g + (int32_t)(at - (uint32_t)r.index * plan.g);
+    r.index = (int32_t)plan.g(at);
+    r.head = (int32_t)(c.kvh * plan.g.n + at - r.index * plan.g.n);
     r.token = r.index < k.ntok ? k.tok0 + r.index : -1;
     return r;
 }
@@ -1114,16 +1114,17 @@ cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* 
     plan.score = make_score_map(p);
     plan.counters = static_cast<int32_t*>(workspace);
     plan.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-    plan.g = p.hq / p.hk;
-    plan.seqs_a_tile = std::max(1, kRows / plan.g);
-    plan.tiles_a_seq = (int32_t)ceil_div(plan.g, kRows);
+    const int g = p.hq / p.hk;
+    plan.g = make_row_divide(g);
+    plan.seqs_a_tile = std::max(1, kRows / g);
+    plan.tiles_a_seq = (int32_t)ceil_div(g, kRows);
     plan.min_units = 1;
 
     // Many rows a key go to the tile kernel: all of a ragged batch, or the
     // prefixes of a shared one (a window cuts prefixes row by row: the row
     // kernel leaves out what nobody sees).
     const int64_t entities = p.group_start ? p.n_groups : p.n_seqs;
-    if (p.tokens * plan.g >= kTileRowsFrom * entities && tiles_can_run(p, dtype) &&
+    if (p.tokens * g >= kTileRowsFrom * entities && tiles_can_run(p, dtype) &&
         !(p.group_start && p.window > 0)) {
         float* prefix_o = nullptr;
         float* prefix_ml = nullptr;

@@ -13,16 +13,27 @@
 
 namespace arops {
 
-// Shared-memory operand: start address, leading and stride byte offsets, all in
-// units of 16 bytes; bit 46 is the descriptor version of this architecture,
-// 2 at bit 61 the 128-byte swizzle.
+// Shared-memory operand: start address (bit 0), leading (bit 16) and stride (bit
+// 32) byte offsets, all in units of 16 bytes; bit 46 is the descriptor version
+// of this architecture, 2 at bit 61 the 128-byte swizzle.
 //   K contiguous: the stride offset steps 8 rows (1024); 64 values of K a row.
 //   M/N contiguous: the stride offset steps 8 values of K (1024), the leading
 //   offset 64 values of M/N.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t leading, uint32_t stride)
+// The address and leading offset fill the low word, the rest the high word.
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t leading)
 {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(leading >> 4) << 16) |
-           ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return ((addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
+
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Instruction word of kind::f16 with bf16 operands and fp32 sums: D format at
@@ -34,25 +45,28 @@ __host__ __device__ constexpr uint32_t mma_word(int m, int n, bool b_n_major)
            ((uint32_t)(n / 8) << 17) | ((uint32_t)(m / 16) << 24);
 }
 
-// D (tensor memory) = A B + (accumulate ? D : 0), both operands in shared memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+// D (tensor memory) = A B + (accumulate ? D : 0), both operands in shared
+// memory, given by the low words of their descriptors.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t word,
                                           bool accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(word), "r"((uint32_t)accumulate), "n"(kOperandHigh)
         : "memory");
 }
 
 // The same with A in tensor memory (two values of K a 32-bit column).
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t word,
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t word,
                                           bool accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(word), "r"((uint32_t)accumulate), "n"(kOperandHigh)
         : "memory");
 }
 
@@ -133,6 +147,28 @@ __device__ __forceinline__ void tc_store32(uint32_t addr, const uint32_t* r)
         "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_load16(uint32_t* r, uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
         : "memory");
 }
 

@@ -27,6 +27,7 @@
 // arrive joins the parts in their order along the keys, so arrival changes no
 // bit.  No CTA waits for another.
 #include "attention_common.cuh"
+#include <stdlib.h>
 
 namespace arops {
 namespace {
@@ -528,6 +529,113 @@ __device__ __forceinline__ void store_result(const AttentionParams& p, const Row
                    plan.vec_out);
 }
 
+// Joins the parts of CTAs cta0 .. cta1 in their order: 2^(m_x - m) O_x summed
+// over x, likewise l.  Latency is all that counts here (a part comes out of
+// L2), so a thread takes its share of the tile's columns of four parts at once.
+template <typename T, int DP, bool SHARED>
+__device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const RowOf* row_at,
+                           int32_t cta0, int32_t cta1, float (*row_m)[kRows],
+                           float (*row_l)[kRows], float* weights)
+{
+    constexpr int kItems = kRows * DP / 4 / kRowThreads;
+    constexpr int kMost = 64;  // parts whose weights are in shared memory at a time
+    auto part_of = [&](int32_t x) {
+        return plan.parts + ((int64_t)x * 2 + (x == cta0 ? 1 : 0)) * part_floats(DP);
+    };
+    const int row = threadIdx.x % kRows, lead = threadIdx.x / kRows;
+    constexpr int kLeads = kRowThreads / kRows;
+    // every row's m and l: kLeads threads a row, then theirs joined
+    float m = -INFINITY, l = 0.0f;
+    if (row_at[row].token >= 0) {
+        for (int32_t x = cta0 + lead; x <= cta1; x += 4 * kLeads) {
+            float mx[4], lx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = x + i * kLeads <= cta1;
+                const float* src = part_of(in ? x + i * kLeads : x) + kRows * DP + row;
+                mx[i] = in ? __ldcg(src) : -INFINITY;
+                lx[i] = in ? __ldcg(src + kRows) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float mn = fmaxf(m, mx[i]);
+                if (mx[i] != -INFINITY)
+                    l = (m == -INFINITY ? 0.0f : l * exp2_fast(m - mn)) +
+                        lx[i] * exp2_fast(mx[i] - mn);
+                m = mn;
+            }
+        }
+    }
+    float* lead_m = weights;
+    float* lead_l = weights + kRowThreads;
+    lead_m[threadIdx.x] = m;
+    lead_l[threadIdx.x] = l;
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kLeads; ++i)
+            m = fmaxf(m, lead_m[i * kRows + row]);
+#pragma unroll
+        for (int i = 0; i < kLeads; ++i)
+            if (lead_m[i * kRows + row] != -INFINITY)
+                l += lead_l[i * kRows + row] * exp2_fast(lead_m[i * kRows + row] - m);
+        row_m[0][row] = m;
+        row_l[0][row] = l;
+    }
+    float sum[kItems][4];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.0f;
+    for (int32_t x0 = cta0; x0 <= cta1; x0 += kMost) {
+        const int n = min(kMost, cta1 - x0 + 1);
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * kRows; i += kRowThreads) {
+            const int r = i % kRows;
+            const float mx = row_at[r].token >= 0
+                                 ? __ldcg(part_of(x0 + i / kRows) + kRows * DP + r)
+                                 : -INFINITY;
+            weights[i] = mx == -INFINITY ? 0.0f : exp2_fast(mx - row_m[0][r]);
+        }
+        __syncthreads();
+        for (int y = 0; y < n; y += 4) {
+            float4 v[4][kItems];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float* src = part_of(x0 + min(y + j, n - 1));
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int idx = threadIdx.x + i * kRowThreads;
+                    v[j][i] = y + j < n && row_at[idx / (DP / 4)].token >= 0
+                                  ? __ldcg(reinterpret_cast<const float4*>(src) + idx)
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int r = (threadIdx.x + i * kRowThreads) / (DP / 4);
+                    const float f = y + j < n ? weights[(y + j) * kRows + r] : 0.0f;
+                    sum[i][0] = fmaf(v[j][i].x, f, sum[i][0]);
+                    sum[i][1] = fmaf(v[j][i].y, f, sum[i][1]);
+                    sum[i][2] = fmaf(v[j][i].z, f, sum[i][2]);
+                    sum[i][3] = fmaf(v[j][i].w, f, sum[i][3]);
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int idx = threadIdx.x + i * kRowThreads;
+        const RowOf r = row_at[idx / (DP / 4)];
+        const int e = idx % (DP / 4) * 4;
+        if (r.token >= 0 && e < p.head_dim)
+            store_result<T, DP, SHARED>(p, plan, r, e, sum[i], row_m[0][idx / (DP / 4)],
+                                        row_l[0][idx / (DP / 4)]);
+    }
+}
+
 template <typename T, int DP, bool VEC, bool FULL, bool SHARED>
 __global__ void __launch_bounds__(kRowThreads, RowTraits<T, DP>::kCtas)
 attention_rows_kernel(const __grid_constant__ AttentionParams p,
@@ -663,6 +771,27 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
 
         // -- the tile's queries, and this lane's two rows ----------------------
         __syncthreads();  // the last pair's use of shared memory is over
+        // keys and values first: their way is the longest.  Stages are filled
+        // ahead; a page is looked up one block before its copy.
+        bool bad_page = false;
+        int32_t issue = u0;
+        KeyBlock nb = key_block<SHARED>(p, c, k, u0, warp);
+        int64_t noff = key_offset(p, nb, c.kvh, lane, bad_page);
+        auto issue_next = [&]() {
+            if (issue < u1) {
+                load_block<T, DP, VEC>(p, ring + (issue - u0) % R::kStages * R::kStage, noff, lane);
+                ++issue;
+                if (issue < u1) {
+                    nb = key_block<SHARED>(p, c, k, issue, warp);
+                    noff = key_offset(p, nb, c.kvh, lane, bad_page);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < R::kStages - 1; ++i)
+            issue_next();
+
         if (threadIdx.x < kRows)
             row_at[threadIdx.x] = row_of(k, plan, c, threadIdx.x);
         __syncthreads();
@@ -723,27 +852,6 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
         for (int n = 0; n < DP / 8; ++n)
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-        bool bad_page = false;
-
-        // stages are filled ahead; a page is looked up one block before its copy
-        int32_t issue = u0;
-        KeyBlock nb = key_block<SHARED>(p, c, k, u0, warp);
-        int64_t noff = key_offset(p, nb, c.kvh, lane, bad_page);
-        auto issue_next = [&]() {
-            if (issue < u1) {
-                load_block<T, DP, VEC>(p, ring + (issue - u0) % R::kStages * R::kStage, noff, lane);
-                ++issue;
-                if (issue < u1) {
-                    nb = key_block<SHARED>(p, c, k, issue, warp);
-                    noff = key_offset(p, nb, c.kvh, lane, bad_page);
-                }
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < R::kStages - 1; ++i)
-            issue_next();
-
         for (int32_t u = u0; u < u1; ++u) {
             cp_async_wait<R::kStages - 2>();
             __syncwarp();
@@ -974,48 +1082,9 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                 }
             }
             __syncthreads();
-            if (last_flag) {
-                const float* first = plan.parts + ((int64_t)cta0 * 2 + 1) * part_floats(DP);
-                auto part_of = [&](int32_t x) {
-                    return x == cta0 ? first : plan.parts + (int64_t)x * 2 * part_floats(DP);
-                };
-                if (threadIdx.x < kRows &&
-                    row_at[threadIdx.x].token >= 0) {
-                    const int row = threadIdx.x;
-                    float mm = -INFINITY, ll = 0.0f;
-                    for (int32_t x = cta0; x <= cta1; ++x)
-                        mm = fmaxf(mm, __ldcg(part_of(x) + kRows * DP + row));
-                    for (int32_t x = cta0; x <= cta1; ++x) {
-                        const float mx = __ldcg(part_of(x) + kRows * DP + row);
-                        if (mx != -INFINITY)
-                            ll += __ldcg(part_of(x) + kRows * DP + kRows + row) *
-                                  exp2_fast(mx - mm);
-                    }
-                    row_m[0][row] = mm;
-                    row_l[0][row] = ll;
-                }
-                __syncthreads();
-                for (int idx = threadIdx.x; idx < kRows * DP / 4; idx += kRowThreads) {
-                    const int row = idx / (DP / 4), e = idx % (DP / 4) * 4;
-                    const RowOf r = row_at[row];
-                    if (r.token < 0 || e >= p.head_dim)
-                        continue;
-                    const float mm = row_m[0][row], ll = row_l[0][row];
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int32_t x = cta0; x <= cta1; ++x) {
-                        const float* src = part_of(x);
-                        const float mx = __ldcg(src + kRows * DP + row);
-                        const float4 v =
-                            __ldcg(reinterpret_cast<const float4*>(src + row * DP + e));
-                        const float f = mx == -INFINITY ? 0.0f : exp2_fast(mx - mm);
-                        sum[0] += v.x * f;
-                        sum[1] += v.y * f;
-                        sum[2] += v.z * f;
-                        sum[3] += v.w * f;
-                    }
-                    store_result<T, DP, SHARED>(p, plan, r, e, sum, mm, ll);
-                }
-            }
+            if (last_flag)
+                join_parts<T, DP, SHARED>(p, plan, row_at, cta0, cta1, row_m, row_l,
+                                          reinterpret_cast<float*>(smem));
         }
 
         // -- on along the line -------------------------------------------------
@@ -1118,7 +1187,7 @@ cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* 
     plan.g = make_row_divide(g);
     plan.seqs_a_tile = std::max(1, kRows / g);
     plan.tiles_a_seq = (int32_t)ceil_div(g, kRows);
-    plan.min_units = 1;
+    plan.min_units = getenv("MINU") ? atoi(getenv("MINU")) : 1;
 
     // Many rows a key go to the tile kernel: all of a ragged batch, or the
     // prefixes of a shared one (a window cuts prefixes row by row: the row

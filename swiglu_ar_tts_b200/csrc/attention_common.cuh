@@ -139,8 +139,7 @@ __device__ __forceinline__ void ragged_range(const AttentionParams& p, const Rag
 // (m, l) of every (sequence, head) there; otherwise it writes p.out.
 bool tiles_can_run(const AttentionParams& p, arops_dtype dtype);
 size_t tile_part_bytes(int dp);
-cudaError_t launch_attention_tiles(const AttentionParams& p, int32_t* counters, float* parts,
-                                   float* prefix_o, float* prefix_ml, int sm_count,
-                                   cudaStream_t stream);
+cudaError_t launch_attention_tiles(const AttentionParams& p, float* parts, float* prefix_o,
+                                   float* prefix_ml, int sm_count, cudaStream_t stream);
 
 }  // namespace arops

@@ -33,13 +33,15 @@ namespace {
 constexpr int kSubRows = 128;
 constexpr int kTileRows = 2 * kSubRows;
 constexpr int kTileUnit = 128;  // keys
-constexpr int kTileThreads = 384;
+constexpr int kTileThreads = 512;
 constexpr int kTileWarps = kTileThreads / 32;
 // Keys whose weights are handed to the products first, the rest follow: the
 // products of the first run under the exponentials of the rest.
 constexpr int kFirstKeys = 96;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
+constexpr int kQueryWarp = 10;   // and 11
+constexpr int kResultWarp = 12;  // to 15
 
 // Largest grid: the workspace holds four partial results a CTA.
 constexpr int kMaxTileCtas = 160;
@@ -55,19 +57,24 @@ struct TileTraits {
     static constexpr int kSlot = kTileUnit * DP * 2;     // keys or values of a unit
     static constexpr int kQ = kSubRows * DP * 2;         // of a sub-tile
     static constexpr int kSlots = DP == 128 ? 4 : 8;     // 128 KB
-    static constexpr int kStage = kSubRows * 128;        // results of a sub-tile, 64 columns
-    static constexpr int kSmem = 2 * kQ + kSlots * kSlot + 2 * kStage + 1024;  // + alignment
+    static constexpr int kStage = kSubRows * DP * 2;     // results of a sub-tile
     static constexpr uint32_t kS = 0, kO = 2 * kTileUnit;  // columns: S_w at kS + 128 w
+};
+
+// A pair that CTA cta0 begins and leaves unfinished; cta1 < cta0: none.
+struct TileSplit {
+    int32_t tok0, ntok, sub, kvh, cta1;
 };
 
 struct TilePlan {
     ScoreMap score;
-    int32_t* counters;
+    TileSplit* splits;  // one a CTA
     float* parts;
     float* prefix_o;    // shared prefixes: results go here, not to out
     float* prefix_ml;
     RowDivide g;        // query heads a key head
     int32_t box;        // keys of one tensor-map copy
+    bool q_map;         // queries by tensor-map copies
 };
 
 struct TileCursor {
@@ -214,24 +221,53 @@ struct TileWalk {
     int64_t place;    // of its unit 0
 };
 
+// One pair's units of a CTA's share, as the roles see it.
+struct TilePiece {
+    int32_t tok0, ntok, len, bidir, lo;
+    int32_t sub, kvh;
+    int32_t u0, u1;          // units of the share; u0 == u1: the end
+    int32_t a[2], b[2];      // of each sub-tile: [a, b)
+    int32_t cta0, cta1;      // the pair's CTAs
+    int32_t whole;
+    const int32_t* table;
+};
+
+constexpr int kPieces = 4;
+
 // The CTA's barriers and flags in shared memory.
 template <int DP>
 struct TileShared {
     uint64_t full[TileTraits<DP>::kSlots];
     uint64_t empty[TileTraits<DP>::kSlots];
-    uint64_t tail;      // a copy of values that reaches past the sequence's end
+    uint64_t piece_full[kPieces];
+    uint64_t piece_empty[kPieces];
+    uint64_t tail;        // a copy of values that reaches past the sequence's end
     uint64_t q_ready[2];
+    uint64_t q_free[2];   // a piece's last product with Q_w is done
     uint64_t s_full[2];
     uint64_t p_ready[2][2];
     uint64_t o_done[2];
+    uint64_t ml_ready[2]; // a piece's m and l are in shared memory
+    uint64_t o_free[2];   // a piece's O_w, m and l have been read
     uint64_t drain;
+    TilePiece pieces[kPieces];
+    float m[2][kSubRows], l[2][kSubRows];
     uint32_t tmem;
-    int stop;           // a wait ran out: everybody leaves
-    int last[2];
+    int stop;             // a wait ran out: everybody leaves
     int64_t sums[kTileWarps];
     int64_t found_before;  // line in front of the found entity, per key head
     TileCursor found;
 };
+
+// All of a CTA's shared memory; its operands lie on 1024-byte boundaries, which
+// is where dynamic shared memory begins in a kernel without any other (checked
+// by the kernel).
+template <int DP>
+constexpr int tile_smem()
+{
+    using R = TileTraits<DP>;
+    return 2 * R::kQ + R::kSlots * R::kSlot + R::kStage + (int)sizeof(TileShared<DP>);
+}
 
 // Waits for `parity` of `bar`; false once anybody's wait has run out.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* stop, unsigned* err)
@@ -254,25 +290,47 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* st
     }
 }
 
+// A warp's wait: all lanes go on together, or none does.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* stop, unsigned* err)
+{
+    return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, stop, err));
+}
+
+// A role's way through the pieces (a warp).
+template <int DP>
+struct PieceReader {
+    uint32_t n = 0;
+    __device__ __forceinline__ bool next(TileShared<DP>& sh, TilePiece& t, unsigned* err)
+    {
+        const uint32_t s = n % kPieces;
+        if (!warp_wait(&sh.piece_full[s], (n / kPieces) & 1, &sh.stop, err))
+            return false;
+        t = sh.pieces[s];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(smem_addr(&sh.piece_empty[s]));
+        ++n;
+        return t.u0 < t.u1;
+    }
+};
+
 // ---------------------------------------------------------------------------
-// Copies (one warp).
+// Copies of keys and values (one warp).
 // ---------------------------------------------------------------------------
-template <int DP, bool SHARED>
+template <int DP>
 __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                                const CUtensorMap* kmap, const CUtensorMap* vmap,
-                               unsigned char* slots, TileShared<DP>& sh, TileCursor c, int64_t begin,
-                               int64_t end, int lane)
+                               unsigned char* slots, TileShared<DP>& sh, int lane)
 {
     using R = TileTraits<DP>;
     const int boxes = kTileUnit / plan.box;
     uint32_t n = 0;      // slots filled
     uint32_t tails = 0;  // copies waited for here
     bool ok = true;
-    TileWalk walk(c, begin, end);
-    TileSpan t;
-    int32_t u0, u1;
-    while (ok && walk.next<SHARED>(p, plan, t, u0, u1)) {
-        for (int32_t u = u0; ok && u < u1; ++u) {
+    PieceReader<DP> reader;
+    TilePiece t;
+    while (ok && reader.next(sh, t, p.err)) {
+        for (int32_t u = t.u0; ok && u < t.u1; ++u) {
             const int32_t key0 = t.lo + u * kTileUnit;
             const int32_t key = key0 + lane * plan.box;
             // a copy of a page that does not exist brings zeros
@@ -287,14 +345,12 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                 }
             }
             const bool tail = t.len - key0 < kTileUnit;
-#pragma unroll
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
                 const uint32_t s = n % R::kSlots;
-                ok = wait_for(&sh.empty[s], ((n / R::kSlots) & 1) ^ 1, &sh.stop, p.err);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
+                ok = warp_wait(&sh.empty[s], ((n / R::kSlots) & 1) ^ 1, &sh.stop, p.err);
+                if (!ok)
                     break;
-                }
                 unsigned char* dst = slots + s * R::kSlot;
                 const bool clean = kv == 1 && tail;
                 const uint32_t bar = smem_addr(clean ? &sh.tail : &sh.full[s]);
@@ -305,18 +361,16 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
 #pragma unroll
                     for (int h = 0; h < R::kHalves; ++h)
                         tensor_load4(smem_addr(dst) + h * (kTileUnit * 128) + lane * plan.box * 128,
-                                     kv ? vmap : kmap, bar, h * 64, slot, walk.pair.kvh,
-                                     page);
+                                     kv ? vmap : kmap, bar, h * 64, slot, t.kvh, page);
                 }
+                ++n;
                 if (clean) {
                     // slots behind the sequence's end may hold anything, and 0
                     // times a NaN is one: their values become zeros
-                    ok = wait_for(&sh.tail, tails & 1, &sh.stop, p.err);
+                    ok = warp_wait(&sh.tail, tails & 1, &sh.stop, p.err);
                     ++tails;
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
+                    if (!ok)
                         break;
-                    }
                     const int first = max(t.len - key0, 0);
                     for (int i = first * 8 + lane; i < kTileUnit * 8; i += 32)
 #pragma unroll
@@ -328,7 +382,6 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                     if (lane == 0)
                         mbar_arrive(smem_addr(&sh.full[s]));
                 }
-                ++n;
             }
         }
     }
@@ -340,118 +393,8 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
 }
 
 // ---------------------------------------------------------------------------
-// Products (one warp; one thread of it issues).
+// Queries (one warp a sub-tile; sub-tile 0's also makes the pieces).
 // ---------------------------------------------------------------------------
-template <int DP, bool SHARED>
-__device__ void tile_mma_role(const AttentionParams& p, const TilePlan& plan,
-                              const unsigned char* q, const unsigned char* slots,
-                              TileShared<DP>& sh, TileCursor c, int64_t begin, int64_t end)
-{
-    using R = TileTraits<DP>;
-    constexpr uint32_t kWordS = mma_word(kSubRows, kTileUnit, false);
-    constexpr uint32_t kWordO = mma_word(kSubRows, DP, true);
-    const uint32_t tmem = sh.tmem;
-    // keys and queries: K (head_dim) contiguous, one 64-value block behind the
-    // other; values: N (head_dim) contiguous, the leading offset between blocks
-    const uint32_t q_low = operand_low(smem_addr(q), 16);
-    const uint32_t k_low = operand_low(smem_addr(slots), 16);
-    const uint32_t v_low = operand_low(smem_addr(slots), kTileUnit * 128);
-    uint32_t used = 0;                   // slots consumed
-    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, &sh.stop, p.err));
-    };
-    TileWalk walk(c, begin, end);
-    TileSpan t;
-    int32_t u0, u1;
-    while (walk.next<SHARED>(p, plan, t, u0, u1)) {
-        int32_t a[2], b[2];  // the sub-tiles' units of this share
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            a[w] = max(t.jlo[w], u0);
-            b[w] = min(t.jhi[w], u1);
-        }
-        // slots in order: keys u0, values u0, keys u0 + 1, ...
-        for (int32_t u = u0 - 1; u < u1; ++u) {
-            uint32_t vs = 0, ks = 0;
-            if (u >= u0) {
-                vs = used % R::kSlots;
-                if (!wait(&sh.full[vs], (used / R::kSlots) & 1))
-                    return;
-                ++used;
-            }
-            if (u + 1 < u1) {
-                ks = used % R::kSlots;
-                if (!wait(&sh.full[ks], (used / R::kSlots) & 1))
-                    return;
-                ++used;
-            }
-            const uint32_t vb = v_low + vs * (R::kSlot >> 4);
-            const uint32_t kb = k_low + ks * (R::kSlot >> 4);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const uint32_t o = tmem + R::kO + w * DP;
-                const uint32_t s = tmem + R::kS + w * kTileUnit;
-                if (u >= a[w] && u < b[w]) {  // O_w (+)= P_w V
-                    if (!wait(&sh.p_ready[w][0], pn[w] & 1))
-                        return;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kFirstKeys / 16; ++k)
-                            tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO,
-                                      u > a[w] || k > 0);
-                    }
-                    __syncwarp();
-                    if (!wait(&sh.p_ready[w][1], pn[w] & 1))
-                        return;
-                    tc_fence_after();
-                    ++pn[w];
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = kFirstKeys / 16; k < kTileUnit / 16; ++k)
-                            tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO, true);
-                        tc_commit(smem_addr(&sh.o_done[w]));
-                    }
-                    __syncwarp();
-                }
-                if (u + 1 >= a[w] && u + 1 < b[w]) {  // the next S_w = Q_w K^T
-                    if (u + 1 == a[w]) {
-                        if (!wait(&sh.q_ready[w], qn[w] & 1))
-                            return;
-                        ++qn[w];
-                        tc_fence_after();
-                    }
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < DP / 16; ++k) {
-                            const uint32_t off = ((k / 4) * (kTileUnit * 128) + (k % 4) * 32) >> 4;
-                            tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off, kb + off, kWordS, k > 0);
-                        }
-                        tc_commit(smem_addr(&sh.s_full[w]));
-                    }
-                    __syncwarp();
-                }
-            }
-            if (elect_one()) {
-                if (u >= u0)
-                    tc_commit(smem_addr(&sh.empty[vs]));
-                if (u + 1 < u1)
-                    tc_commit(smem_addr(&sh.empty[ks]));
-            }
-            __syncwarp();
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Softmax (four warps a sub-tile, a row a thread).
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void sub_tile_barrier(int w)
-{
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
-}
-
 // (token, head) of rows that a thread takes `step` apart.
 struct RowStep {
     uint32_t tok, head, g, dt, dh;
@@ -473,28 +416,42 @@ struct RowStep {
     }
 };
 
-// The sub-tile's query rows into shared memory (asynchronous copies).
+// A sub-tile's 128 query rows, swizzled as a tensor-map copy leaves them: by
+// such a copy where the heads of a token divide the 128 rows, else 16 bytes at
+// a time.
 template <int DP>
-__device__ __forceinline__ void load_q_rows(const AttentionParams& p, const RowDivide& g,
-                                            const TileSpan& t, const TileCursor& c, int w,
-                                            unsigned char* q, int tid)
+__device__ __forceinline__ void load_queries(const AttentionParams& p, const TilePlan& plan,
+                                             const CUtensorMap* qmap, const TilePiece& t, int w,
+                                             unsigned char* q, uint64_t* ready, int lane)
 {
+    using R = TileTraits<DP>;
+    const uint32_t row0 = (uint32_t)t.sub * kTileRows + w * kSubRows;
+    if (plan.q_map) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(ready), R::kQ);
+#pragma unroll
+            for (int h = 0; h < R::kHalves; ++h)
+                tensor_load3(smem_addr(q) + h * (kSubRows * 128), qmap, smem_addr(ready), h * 64,
+                             (int32_t)(t.kvh * plan.g.n), (int32_t)(t.tok0 + plan.g(row0)));
+        }
+        __syncwarp();
+        return;
+    }
     constexpr int kChunks = DP / 8;
-    constexpr int kStep = 128 / kChunks;
-    const int chunk = tid % kChunks;
-    int row = tid / kChunks;
+    constexpr int kStep = 32 / kChunks;
+    const int chunk = lane % kChunks;
+    int row = lane / kChunks;
     const bool used = chunk < p.head_dim / 8;
-    RowStep r(g, (uint32_t)c.sub * kTileRows + w * kSubRows + row, kStep);
-    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.q) +
-                                t.tok0 * p.q_stride + (int64_t)c.kvh * g.n * p.head_dim +
-                                chunk * 8;
+    RowStep r(plan.g, row0 + row, kStep);
+    const __nv_bfloat16* all = static_cast<const __nv_bfloat16*>(p.q);
+    const __nv_bfloat16* base =
+        all + t.tok0 * p.q_stride + (int64_t)t.kvh * plan.g.n * p.head_dim + chunk * 8;
     const uint32_t dst = smem_addr(q) + (chunk / 8) * (kSubRows * 128);
 #pragma unroll 4
     for (int i = 0; i < kSubRows / kStep; ++i) {
         const bool ok = r.tok < (uint32_t)t.ntok && used;
         const __nv_bfloat16* src =
-            ok ? base + (int64_t)r.tok * p.q_stride + r.head * p.head_dim
-               : static_cast<const __nv_bfloat16*>(p.q);
+            ok ? base + (int64_t)r.tok * p.q_stride + r.head * p.head_dim : all;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                          dst + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)),
                      "l"(src), "r"(ok ? 16u : 0u)
@@ -502,61 +459,205 @@ __device__ __forceinline__ void load_q_rows(const AttentionParams& p, const RowD
         row += kStep;
         r.next();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_async_proxy();
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(smem_addr(ready));
 }
 
-// 64 columns of a sub-tile's results, a row a thread, divided by l: through
-// shared memory, so that eight threads store a row's 128 bytes together.
 template <int DP, bool SHARED>
-__device__ __forceinline__ void emit_columns(const AttentionParams& p, const TilePlan& plan,
-                                             const TileSpan& t, const TileCursor& c,
-                                             const uint32_t (&o)[64], int col, float m, float l,
-                                             unsigned char* stage, int w, int tid)
+__device__ void tile_query_role(const AttentionParams& p, const TilePlan& plan,
+                                const CUtensorMap* qmap, unsigned char* q, TileShared<DP>& sh,
+                                const TileCursor& from, int64_t begin, int64_t end, int64_t share,
+                                int w, int lane)
 {
-    const uint32_t row0 = (uint32_t)c.sub * kTileRows + w * kSubRows;
-    if constexpr (SHARED) {
-        const RowStep r(plan.g, row0 + tid, 1);
-        if (r.tok < (uint32_t)t.ntok) {
-            const int64_t at = (int64_t)(t.tok0 + r.tok) * p.hq + c.kvh * plan.g.n + r.head;
-            float4* dst = reinterpret_cast<float4*>(plan.prefix_o + at * DP + col);
+    uint32_t loaded = 0;
+    auto load = [&](const TilePiece& t) {
+        if (w ? t.a[1] >= t.b[1] : t.a[0] >= t.b[0])
+            return true;
+        if (!warp_wait(&sh.q_free[w], (loaded & 1) ^ 1, &sh.stop, p.err))
+            return false;
+        ++loaded;
+        load_queries<DP>(p, plan, qmap, t, w, q, &sh.q_ready[w], lane);
+        return true;
+    };
+    TilePiece t;
+    if (w == 1) {
+        PieceReader<DP> reader;
+        while (reader.next(sh, t, p.err))
+            if (!load(t))
+                return;
+        return;
+    }
+    TileWalk walk(from, begin, end);
+    bool more = true;
+    for (uint32_t n = 0; more; ++n) {
+        TileSpan s;
+        t.u0 = t.u1 = 0;
+        more = walk.next<SHARED>(p, plan, s, t.u0, t.u1);
+        if (more) {
+            t.tok0 = s.tok0;
+            t.ntok = s.ntok;
+            t.len = s.len;
+            t.bidir = s.bidir;
+            t.lo = s.lo;
+            t.table = s.table;
+            t.sub = walk.pair.sub;
+            t.kvh = walk.pair.kvh;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-            if (col == 0)
-                *reinterpret_cast<float2*>(plan.prefix_ml + at * 2) = make_float2(m, l);
+            for (int i = 0; i < 2; ++i) {
+                t.a[i] = max(s.jlo[i], t.u0);
+                t.b[i] = min(s.jhi[i], t.u1);
+            }
+            t.cta0 = (int32_t)(walk.place / share);
+            t.cta1 = (int32_t)((walk.place + s.units - 1) / share);
+            t.whole = t.u0 == 0 && t.u1 == s.units;
+        } else {
+            t.u0 = t.u1 = 0;
         }
-    } else {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float y[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                y[x] = l == 0.0f ? 0.0f : __uint_as_float(o[8 * e + x]) * inv;
-            *reinterpret_cast<uint4*>(stage + tid * 128 + ((e ^ (tid & 7)) << 4)) =
-                Vec<__nv_bfloat16>::pack(y);
+        const uint32_t slot = n % kPieces;
+        if (!warp_wait(&sh.piece_empty[slot], ((n / kPieces) & 1) ^ 1, &sh.stop, p.err))
+            return;
+        if (lane == 0) {
+            sh.pieces[slot] = t;
+            mbar_arrive(smem_addr(&sh.piece_full[slot]));
         }
-        sub_tile_barrier(w);
-        const int chunk = tid & 7;
-        int row = tid >> 3;
-        RowStep r(plan.g, row0 + row, 16);
-        __nv_bfloat16* base = static_cast<__nv_bfloat16*>(p.out) +
-                              ((int64_t)t.tok0 * p.hq + c.kvh * plan.g.n) * p.head_dim + col +
-                              chunk * 8;
-        const bool used = col + chunk * 8 < p.head_dim;
-#pragma unroll
-        for (int i = 0; i < kSubRows / 16; ++i) {
-            const uint4 v =
-                *reinterpret_cast<const uint4*>(stage + row * 128 + ((chunk ^ (row & 7)) << 4));
-            if (used && r.tok < (uint32_t)t.ntok)
-                *reinterpret_cast<uint4*>(base + ((int64_t)r.tok * p.hq + r.head) * p.head_dim) = v;
-            row += 16;
-            r.next();
-        }
-        sub_tile_barrier(w);
+        __syncwarp();
+        if (more && !load(t))
+            return;
     }
 }
 
+// ---------------------------------------------------------------------------
+// Products (one warp; one thread of it issues).
+// ---------------------------------------------------------------------------
+template <int DP>
+__device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
+                              const unsigned char* slots, TileShared<DP>& sh)
+{
+    using R = TileTraits<DP>;
+    constexpr uint32_t kWordS = mma_word(kSubRows, kTileUnit, false);
+    constexpr uint32_t kWordO = mma_word(kSubRows, DP, true);
+    const uint32_t tmem = sh.tmem;
+    // keys and queries: K (head_dim) contiguous, one 64-value block behind the
+    // other; values: N (head_dim) contiguous, the leading offset between blocks
+    const uint32_t q_low = operand_low(smem_addr(q), 16);
+    const uint32_t k_low = operand_low(smem_addr(slots), 16);
+    const uint32_t v_low = operand_low(smem_addr(slots), kTileUnit * 128);
+    uint32_t used = 0;                     // slots consumed
+    uint32_t qn[2] = {0, 0}, on[2] = {0, 0}, pn[2] = {0, 0};  // waits so far
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return warp_wait(bar, parity, &sh.stop, p.err);
+    };
+    // The units of all pieces form one line: under the softmax of a piece's last
+    // unit the next piece's first S is multiplied.
+    struct Unit {
+        int32_t u, u1, a[2], b[2];
+    };
+    PieceReader<DP> reader;
+    auto next_piece = [&](Unit& n) {
+        TilePiece t;
+        if (!reader.next(sh, t, p.err))
+            return false;
+        n.u = t.u0;
+        n.u1 = t.u1;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            n.a[w] = t.a[w];
+            n.b[w] = t.b[w];
+        }
+        return true;
+    };
+    auto slot = [&](uint32_t& s) {
+        s = used % R::kSlots;
+        const bool ok = wait(&sh.full[s], (used / R::kSlots) & 1);
+        ++used;
+        return ok;
+    };
+    Unit cur, nxt;
+    bool first = true, more = next_piece(nxt);
+    while (first ? more : true) {
+        // slots in order: keys 0, values 0, keys 1, values 1, ...
+        uint32_t vs = 0, ks = 0;
+        if (!first) {
+            cur = nxt;
+            if (nxt.u + 1 < nxt.u1)
+                ++nxt.u;
+            else
+                more = next_piece(nxt);
+            if (!slot(vs))
+                return;
+        }
+        if (more && !slot(ks))
+            return;
+        const uint32_t vb = v_low + vs * (R::kSlot >> 4);
+        const uint32_t kb = k_low + ks * (R::kSlot >> 4);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const uint32_t o = tmem + R::kO + w * DP;
+            const uint32_t s = tmem + R::kS + w * kTileUnit;
+            if (!first && cur.u >= cur.a[w] && cur.u < cur.b[w]) {  // O_w (+)= P_w V
+                // the piece before this one's O_w has been read
+                if (cur.u == cur.a[w] && !wait(&sh.o_free[w], (on[w]++ & 1) ^ 1))
+                    return;
+                if (!wait(&sh.p_ready[w][0], pn[w] & 1))
+                    return;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kFirstKeys / 16; ++k)
+                        tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO,
+                                  cur.u > cur.a[w] || k > 0);
+                }
+                __syncwarp();
+                if (!wait(&sh.p_ready[w][1], pn[w] & 1))
+                    return;
+                tc_fence_after();
+                ++pn[w];
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = kFirstKeys / 16; k < kTileUnit / 16; ++k)
+                        tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO, true);
+                    tc_commit(smem_addr(&sh.o_done[w]));
+                }
+                __syncwarp();
+            }
+            if (more && nxt.u >= nxt.a[w] && nxt.u < nxt.b[w]) {  // the next S_w = Q_w K^T
+                if (nxt.u == nxt.a[w]) {
+                    if (!wait(&sh.q_ready[w], qn[w]++ & 1))
+                        return;
+                    tc_fence_after();
+                }
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        const uint32_t off = ((k / 4) * (kTileUnit * 128) + (k % 4) * 32) >> 4;
+                        tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off, kb + off, kWordS, k > 0);
+                    }
+                    tc_commit(smem_addr(&sh.s_full[w]));
+                    if (nxt.u + 1 == nxt.b[w])
+                        tc_commit(smem_addr(&sh.q_free[w]));
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) {
+            if (!first)
+                tc_commit(smem_addr(&sh.empty[vs]));
+            if (more)
+                tc_commit(smem_addr(&sh.empty[ks]));
+        }
+        __syncwarp();
+        if (!more)
+            return;
+        first = false;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax (four warps a sub-tile, a row a thread).
+// ---------------------------------------------------------------------------
 // A row's scores from its products, in base 2: cap, then bias.
 //   |s| <= cap / 2 in all rows of the warp (a cap is there for outliers): tanh
 //   by its polynomial, 6 operations a pair of keys on the fp32 pipe instead of
@@ -622,83 +723,59 @@ __device__ __forceinline__ void map_row(uint32_t (&s)[kTileUnit], const ScoreMap
 }
 
 template <int DP, bool FULL, bool SHARED>
-__device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan, unsigned char* q,
-                                  unsigned char* stage, TileShared<DP>& sh, const TileCursor& from,
-                                  int64_t begin, int64_t end, int64_t share, int w, int tid)
+__device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan,
+                                  TileShared<DP>& sh, int w, int tid)
 {
     using R = TileTraits<DP>;
     const int lane = tid & 31;
     const uint32_t lanes = (uint32_t)(tid & ~31) << 16;  // the warp's lanes of tensor memory
     const uint32_t s_addr = sh.tmem + lanes + R::kS + w * kTileUnit;
     const uint32_t o_addr = sh.tmem + lanes + R::kO + w * DP;
-    uint32_t sn = 0, on = 0;  // S tiles seen, P V products asked for
-
-    // once a wait has run out a warp does nothing but keep the barriers
-    bool dead = false;
+    uint32_t on = 0;     // units done: S tiles seen, P V products asked for
+    uint32_t ended = 0;  // pieces with units of this sub-tile
+    const float scale = FULL ? 1.0f : plan.score.scale;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        dead = !__all_sync(0xFFFFFFFFu, !dead && wait_for(bar, parity, &sh.stop, p.err));
-        return !dead;
+        return warp_wait(bar, parity, &sh.stop, p.err);
     };
-    // the first tile's queries; later ones are asked for under the last unit of
-    // the tile before
-    TileWalk walk(from, begin, end);
-    TileSpan next_t;
-    int32_t next_u0, next_u1;
-    auto next_queries = [&]() {
-        const bool more = walk.next<SHARED>(p, plan, next_t, next_u0, next_u1);
-        if (more)
-            load_q_rows<DP>(p, plan.g, next_t, walk.pair, w, q, tid);
-        return more;
-    };
-    bool more = next_queries();
-
-    while (more) {
-        const TileSpan t = next_t;
-        const TileCursor c = walk.pair;
-        const int64_t place = walk.place;
-        const int32_t u0 = next_u0, u1 = next_u1;
-        const int32_t a = max(t.jlo[w], u0), b = min(t.jhi[w], u1);
-
-        // this thread's row
-        const RowStep r(plan.g, (uint32_t)c.sub * kTileRows + w * kSubRows + tid, 1);
-        const bool valid = r.tok < (uint32_t)t.ntok;
-        int32_t pos, lo = 0, hi = t.len;
-        if constexpr (SHARED) {
-            bool ignore = false;
-            pos = t.len - 1;
-            if (FULL && valid)
-                pos += clamp_length(__ldg(p.kv_lens + t.tok0 + r.tok),
-                                    p.max_pages * p.map.page_size, ignore);
-        } else {
-            pos = t.len - t.ntok + (int32_t)r.tok;
-            if (valid)
-                visible_keys(pos, t.len, t.bidir, p.window, lo, hi);
-            else
-                hi = INT_MAX;  // nobody reads such a row
-        }
-        const float slope =
-            FULL && p.slopes && valid ? __ldg(p.slopes + c.kvh * plan.g.n + r.head) : 0.0f;
-        const float scale = FULL ? 1.0f : plan.score.scale;
-
-        bool asked = false;  // for the next tile's queries
-        if (a < b) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_addr(&sh.q_ready[w]));
-        }
-        float m = -INFINITY, l = 0.0f;
-        for (int32_t u = a; u < b; ++u) {
-            if (!wait(&sh.s_full[w], sn & 1))
-                break;
-            ++sn;
-            tc_fence_after();
-            if (u + 1 == b) {
-                // Q_w has been read for the last time
-                more = next_queries();
-                asked = true;
+    PieceReader<DP> reader;
+    for (;;) {
+        int32_t key0, a, b, pos, lo = 0, hi;
+        float slope = 0.0f;
+        {
+            TilePiece t;
+            if (!reader.next(sh, t, p.err))
+                return;
+            key0 = t.lo;
+            a = w ? t.a[1] : t.a[0];
+            b = w ? t.b[1] : t.b[0];
+            // this thread's row
+            const RowStep r(plan.g, (uint32_t)t.sub * kTileRows + w * kSubRows + tid, 1);
+            const bool valid = r.tok < (uint32_t)t.ntok;
+            hi = t.len;
+            if constexpr (SHARED) {
+                bool ignore = false;
+                pos = t.len - 1;
+                if (FULL && valid)
+                    pos += clamp_length(__ldg(p.kv_lens + t.tok0 + r.tok),
+                                        p.max_pages * p.map.page_size, ignore);
+            } else {
+                pos = t.len - t.ntok + (int32_t)r.tok;
+                if (valid)
+                    visible_keys(pos, t.len, t.bidir, p.window, lo, hi);
+                else
+                    hi = INT_MAX;  // nobody reads such a row
             }
+            if (FULL && p.slopes && valid)
+                slope = __ldg(p.slopes + t.kvh * plan.g.n + r.head);
+        }
+        if (a >= b)
+            continue;
+        key0 += a * kTileUnit;
+        float m = -INFINITY, l = 0.0f;
+        for (int32_t n = b - a; n > 0; --n, key0 += kTileUnit) {
+            if (!wait(&sh.s_full[w], on & 1))
+                return;
+            tc_fence_after();
             uint32_t s[kTileUnit];
 #pragma unroll
             for (int i = 0; i < kTileUnit; i += 32)
@@ -706,7 +783,6 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
             tc_wait_ld();
             tc_loaded<kTileUnit>(s);
 
-            const int32_t key0 = t.lo + u * kTileUnit;
             if constexpr (FULL)
                 map_row(s, plan.score, slope, pos, key0);
             if (__any_sync(0xFFFFFFFFu, key0 < lo || hi - key0 < kTileUnit)) {
@@ -739,9 +815,9 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                 const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
                 m = mn;
                 l *= f;
-                if (u > a) {
+                if (n < b - a) {
                     if (!wait(&sh.o_done[w], (on - 1) & 1))
-                        break;
+                        return;
                     tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < DP; i += 16) {
@@ -786,102 +862,247 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
             const float2 all = add2(sum[0], sum[1]);
             l += all.x + all.y;
         }
-        if (!asked) {  // no unit of this sub-tile here
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            more = next_queries();
-        }
-        const bool has = a < b && wait(&sh.o_done[w], (on - 1) & 1);
-        tc_fence_after();
+        if (!wait(&sh.o_free[w], (ended & 1) ^ 1))
+            return;
+        ++ended;
+        sh.m[w][tid] = m;
+        sh.l[w][tid] = l;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&sh.ml_ready[w]));
+    }
+}
 
-        // -- results -----------------------------------------------------------
-        const bool whole = u0 == 0 && u1 == t.units;
-        const int32_t cta0 = (int32_t)(place / share);
-        const int32_t cta1 = (int32_t)((place + t.units - 1) / share);
-        auto part_of = [&](int32_t x) {
-            return plan.parts + ((int64_t)x * 4 + (x == cta0 ? 2 : 0) + w) * tile_part_floats(DP);
-        };
-        float* part = part_of(blockIdx.x);
+// ---------------------------------------------------------------------------
+// Results (four warps, a row a thread).
+// ---------------------------------------------------------------------------
+// All four warps agree on `ok`.
+__device__ __forceinline__ bool result_agree(bool ok)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void result_barrier()
+{
+    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+}
+
+// 32 columns of a prefix's results, a row a thread.
+template <int DP>
+__device__ __forceinline__ void store_prefix(const AttentionParams& p, const TilePlan& plan,
+                                             int64_t token, int head, const uint32_t (&o)[32],
+                                             int col, float m, float l)
+{
+    const int64_t at = token * p.hq + head;
+    float4* dst = reinterpret_cast<float4*>(plan.prefix_o + at * DP + col);
 #pragma unroll
-        for (int i = 0; i < DP; i += 64) {
-            uint32_t o[64];
-            if (has) {
-                tc_load32(o, o_addr + i);
-                tc_load32(o + 32, o_addr + i + 32);
-                tc_wait_ld();
-                tc_loaded<64>(o);
-            } else {
+    for (int e = 0; e < 8; ++e)
+        dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+    if (col == 0)
+        *reinterpret_cast<float2*>(plan.prefix_ml + at * 2) = make_float2(m, l);
+}
+
+// 32 values times `by` as 16 pairs of bf16.  (A row that sees no key has O = 0
+// and by = 0.)
+__device__ __forceinline__ void scale_pack(const uint32_t (&o)[32], float by, uint32_t (&y)[16])
+{
+    const float2 f = make_float2(by, by);
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    o[e] = 0;
-            }
-            if (whole) {
-                emit_columns<DP, SHARED>(p, plan, t, c, o, i, m, l, stage, w, tid);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 64; e += 4)
-                    *reinterpret_cast<uint4*>(part + ((i + e) / 4 * kSubRows + tid) * 4) =
-                        make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
-        }
-        if (!whole) {
-            part[kSubRows * DP + tid] = m;
-            part[kSubRows * DP + kSubRows + tid] = l;
-            __threadfence();
-            sub_tile_barrier(w);
-            if (tid == 0) {
-                int32_t* counter = plan.counters + kMaxAttentionCtas + cta0 * 2 + w;
-                const int32_t n = cta1 - cta0 + 1;
-                const int32_t old = atomicAdd(counter, 1);
-                if (old < 0 || old >= n)
-                    record_device_error(p.err, AROPS_DEVICE_ERR_WORKSPACE);
-                sh.last[w] = old == n - 1;
-                if (old == n - 1) {
-                    *counter = 0;
-                    __threadfence();
-                }
-            }
-            sub_tile_barrier(w);
-            const bool join = sh.last[w];
-            sub_tile_barrier(w);  // the flag has been read
-            if (join) {
-                float mm = -INFINITY, ll = 0.0f;
-                for (int32_t x = cta0; x <= cta1; ++x) {
-                    const float mx = __ldcg(part_of(x) + kSubRows * DP + tid);
-                    const float lx = __ldcg(part_of(x) + kSubRows * DP + kSubRows + tid);
-                    const float mn = fmaxf(mm, mx);
-                    if (mx != -INFINITY)
-                        ll = (mm == -INFINITY ? 0.0f : ll * exp2_fast(mm - mn)) +
-                             lx * exp2_fast(mx - mn);
-                    mm = mn;
-                }
+    for (int e = 0; e < 16; ++e) {
+        const float2 x =
+            mul2(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), f);
+        y[e] = pack_bf16x2(x.x, x.y);
+    }
+}
+
+template <int DP, bool SHARED>
+__device__ void tile_result_role(const AttentionParams& p, const TilePlan& plan,
+                                 unsigned char* stage, TileShared<DP>& sh, int tid)
+{
+    using R = TileTraits<DP>;
+    const int lane = tid & 31;
+    const uint32_t lanes = (uint32_t)(tid & ~31) << 16;
+    uint32_t on0 = 0, on1 = 0, ended0 = 0, ended1 = 0;
+    TileSplit split = {0, 0, 0, 0, -1};
+    PieceReader<DP> reader;
+    TilePiece t;
+    for (;;) {
+        // the four warps leave together: one of them alone would leave the
+        // others in a barrier
+        const bool more = reader.next(sh, t, p.err);
+        if (!result_agree(more))
+            break;
+        if (!t.whole && t.u0 == 0)
+            split = {t.tok0, t.ntok, t.sub, t.kvh, t.cta1};
 #pragma unroll 1
-                for (int i = 0; i < DP; i += 64) {
-                    uint32_t o[64];
+        for (int w = 0; w < 2; ++w) {
+            const int32_t units = w ? t.b[1] - t.a[1] : t.b[0] - t.a[0];
+            const bool has = units > 0;
+            float m = -INFINITY, l = 0.0f;
+            if (has) {
+                const uint32_t done = (w ? on1 : on0) + units - 1, piece = w ? ended1 : ended0;
+                if (w) {
+                    on1 += units;
+                    ++ended1;
+                } else {
+                    on0 += units;
+                    ++ended0;
+                }
+                const bool ok = warp_wait(&sh.ml_ready[w], piece & 1, &sh.stop, p.err) &&
+                                warp_wait(&sh.o_done[w], done & 1, &sh.stop, p.err);
+                if (!result_agree(ok))
+                    return;
+                tc_fence_after();
+                m = sh.m[w][tid];
+                l = sh.l[w][tid];
+            }
+            const uint32_t row0 = (uint32_t)t.sub * kTileRows + w * kSubRows;
+            float* part = plan.parts +
+                          ((int64_t)blockIdx.x * 4 + (t.u0 == 0 ? 2 : 0) + w) *
+                              tile_part_floats(DP);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+            for (int i = 0; i < DP; i += 32) {
+                uint32_t o[32];
+                if (has) {
+                    tc_load32(o, sh.tmem + lanes + R::kO + w * DP + i);
+                    tc_wait_ld();
+                    tc_loaded<32>(o);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
+                    for (int e = 0; e < 32; ++e)
                         o[e] = 0;
-                    for (int32_t x = cta0; x <= cta1; ++x) {
-                        const float* src = part_of(x);
-                        const float mx = __ldcg(src + kSubRows * DP + tid);
-                        uint4 v[16];
+                }
+                if (!t.whole) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            v[e] = __ldcg(reinterpret_cast<const uint4*>(
-                                src + ((i / 4 + e) * kSubRows + tid) * 4));
-                        const float fx = mx == -INFINITY ? 0.0f : exp2_fast(mx - mm);
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(part + ((i + e) / 4 * kSubRows + tid) * 4) =
+                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if constexpr (SHARED) {
+                    const RowStep r(plan.g, row0 + tid, 1);
+                    if (r.tok < (uint32_t)t.ntok)
+                        store_prefix<DP>(p, plan, t.tok0 + r.tok, t.kvh * plan.g.n + r.head, o, i,
+                                         m, l);
+                } else {
+                    // to shared memory first, so that eight threads store a
+                    // row's 128 bytes together
+                    uint32_t y[16];
+                    scale_pack(o, inv, y);
+                    unsigned char* dst = stage + i / 64 * (kSubRows * 128) + tid * 128;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint32_t y[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-#pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                o[4 * e + z] = __float_as_uint(fmaf(
-                                    __uint_as_float(y[z]), fx, __uint_as_float(o[4 * e + z])));
-                        }
-                    }
-                    emit_columns<DP, SHARED>(p, plan, t, c, o, i, mm, ll, stage, w, tid);
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(
+                            dst + (((i / 8 % 8 + e) ^ (tid & 7)) << 4)) =
+                            make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                 }
             }
+            if (has) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.o_free[w]));
+            }
+            if (!t.whole) {
+                part[kSubRows * DP + tid] = m;
+                part[kSubRows * DP + kSubRows + tid] = l;
+            } else if constexpr (!SHARED) {
+                result_barrier();
+                const int chunk = tid & 7;
+                int row = tid >> 3;
+                RowStep r(plan.g, row0 + row, 16);
+                const int64_t step = (int64_t)p.hq * p.head_dim;
+                __nv_bfloat16* base = static_cast<__nv_bfloat16*>(p.out) + t.tok0 * step +
+                                      t.kvh * plan.g.n * p.head_dim + chunk * 8;
+                const unsigned char* src = stage + row * 128 + ((chunk ^ (row & 7)) << 4);
+#pragma unroll 4
+                for (int j = 0; j < kSubRows / 16; ++j) {
+                    __nv_bfloat16* dst = base + r.tok * step + r.head * p.head_dim;
+#pragma unroll
+                    for (int h = 0; h < R::kHalves; ++h) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            src + h * (kSubRows * 128) + j * 2048);
+                        if (h * 64 + chunk * 8 < p.head_dim && r.tok < (uint32_t)t.ntok)
+                            *reinterpret_cast<uint4*>(dst + h * 64) = v;
+                    }
+                    r.next();
+                }
+                result_barrier();
+            }
         }
+    }
+    if (tid == 0)
+        plan.splits[blockIdx.x] = split;
+}
+
+// Joins the parts of the pairs that CTAs left unfinished: a block a (CTA,
+// sub-tile, 32 columns), a row a thread, the parts in their order along the
+// keys: O = sum_x 2^(m_x - m) O_x, l likewise.
+template <int DP, bool SHARED>
+__global__ void __launch_bounds__(kSubRows)
+attention_join_kernel(const __grid_constant__ AttentionParams p,
+                      const __grid_constant__ TilePlan plan)
+{
+    pdl_wait();
+    pdl_allow_dependents();
+    const int32_t cta0 = blockIdx.x;
+    const int w = blockIdx.y, col = blockIdx.z * 32, tid = threadIdx.x;
+    const TileSplit t = plan.splits[cta0];
+    if (t.cta1 < cta0)
+        return;
+    const RowStep r(plan.g, (uint32_t)t.sub * kTileRows + w * kSubRows + tid, 1);
+    if (r.tok >= (uint32_t)t.ntok)
+        return;
+    auto part_of = [&](int32_t x) {
+        return plan.parts + ((int64_t)x * 4 + (x == cta0 ? 2 : 0) + w) * tile_part_floats(DP);
+    };
+    float m = -INFINITY, l = 0.0f;
+    uint32_t o[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        o[e] = 0;
+#pragma unroll 2
+    for (int32_t x = cta0; x <= t.cta1; ++x) {
+        const float* src = part_of(x);
+        const float mx = src[kSubRows * DP + tid];
+        const float lx = src[kSubRows * DP + kSubRows + tid];
+        float4 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = *reinterpret_cast<const float4*>(src + ((col / 4 + e) * kSubRows + tid) * 4);
+        const float mn = fmaxf(m, mx);
+        const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
+        const float fx = mx == -INFINITY ? 0.0f : exp2_fast(mx - mn);
+        m = mn;
+        l = l * f + lx * fx;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float y[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                o[4 * e + z] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + z]), f, y[z] * fx));
+        }
+    }
+    if constexpr (SHARED) {
+        store_prefix<DP>(p, plan, t.tok0 + r.tok, t.kvh * plan.g.n + r.head, o, col, m, l);
+    } else {
+        uint32_t y[16];
+        scale_pack(o, l == 0.0f ? 0.0f : 1.0f / l, y);
+        __nv_bfloat16* dst =
+            static_cast<__nv_bfloat16*>(p.out) +
+            ((int64_t)(t.tok0 + r.tok) * p.hq + t.kvh * plan.g.n + r.head) * p.head_dim + col;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e * 8 < p.head_dim)
+                *reinterpret_cast<uint4*>(dst + e * 8) =
+                    make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
     }
 }
 
@@ -890,15 +1111,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 attention_tiles_kernel(const __grid_constant__ AttentionParams p,
                        const __grid_constant__ TilePlan plan,
                        const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap)
+                       const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ CUtensorMap qmap)
 {
     using R = TileTraits<DP>;
-    extern __shared__ unsigned char raw[];
-    __shared__ TileShared<DP> sh;
-    unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* q = smem;
     unsigned char* slots = smem + 2 * R::kQ;
-    unsigned char* stages = slots + R::kSlots * R::kSlot;
+    unsigned char* stage = slots + R::kSlots * R::kSlot;
+    TileShared<DP>& sh = *reinterpret_cast<TileShared<DP>*>(stage + R::kStage);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -906,20 +1127,31 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
             mbar_init(smem_addr(&sh.full[i]), 1);
             mbar_init(smem_addr(&sh.empty[i]), 1);
         }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(smem_addr(&sh.piece_full[i]), 1);
+            // read by the warps of copies, products, softmax, results and the
+            // second one of queries
+            mbar_init(smem_addr(&sh.piece_empty[i]), 1 + 1 + 8 + 4 + 1);
+        }
         mbar_init(smem_addr(&sh.tail), 1);
         mbar_init(smem_addr(&sh.drain), 1);
         for (int w = 0; w < 2; ++w) {
-            mbar_init(smem_addr(&sh.q_ready[w]), 4);
+            mbar_init(smem_addr(&sh.q_ready[w]), 1);
+            mbar_init(smem_addr(&sh.q_free[w]), 1);
             mbar_init(smem_addr(&sh.s_full[w]), 1);
             mbar_init(smem_addr(&sh.p_ready[w][0]), 4);
             mbar_init(smem_addr(&sh.p_ready[w][1]), 4);
             mbar_init(smem_addr(&sh.o_done[w]), 1);
+            mbar_init(smem_addr(&sh.ml_ready[w]), 4);
+            mbar_init(smem_addr(&sh.o_free[w]), 4);
         }
         sh.stop = 0;
         mbar_init_fence();
     }
     pdl_wait();
     pdl_allow_dependents();
+    if (threadIdx.x == 0)
+        plan.splits[blockIdx.x].cta1 = -1;  // none so far
 
     // -- this CTA's share of the line -----------------------------------------
     // `tps` threads count an entity's tiles together
@@ -978,6 +1210,11 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
         total += sh.sums[w];
     }
     const int64_t line = total * p.hk;
+    if ((smem_addr(smem) & 1023u) != 0) {  // does not happen; the swizzle needs it
+        if (threadIdx.x == 0)
+            record_device_error(p.err, kDeviceErrTimeout);
+        return;
+    }
     const int64_t share = max((int64_t)1, (line + gridDim.x - 1) / gridDim.x);
     const int64_t begin = (int64_t)blockIdx.x * share;
     if (begin >= line)
@@ -1033,27 +1270,31 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     const TileCursor c = sh.found;
 
     // Registers: the softmax warps keep a row of 128 scores, the others little.
-    // 256 x 216 + 128 x 72 = 384 x 168, what the launch gave out.
+    // 256 x 192 + 128 x 56 + 128 x 72 = 512 x 128, what the launch gave out.
     if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int w = warp >> 2;
-        tile_softmax_role<DP, FULL, SHARED>(p, plan, q + w * R::kQ, stages + w * R::kStage, sh, c,
-                                            begin, end, share, w, threadIdx.x & 127);
-    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        tile_softmax_role<DP, FULL, SHARED>(p, plan, sh, warp >> 2, threadIdx.x & 127);
+    } else if (warp >= kResultWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        tile_result_role<DP, SHARED>(p, plan, stage, sh, threadIdx.x & 127);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kMmaWarp) {
-            tile_mma_role<DP, SHARED>(p, plan, q, slots, sh, c, begin, end);
+            tile_mma_role<DP>(p, q, slots, sh);
             // every product and every arrival asked for has happened
             if (elect_one())
                 tc_commit(smem_addr(&sh.drain));
             __syncwarp();
             mbar_wait(smem_addr(&sh.drain), 0);
-            __syncwarp();
         } else if (warp == kLoadWarp) {
-            tile_load_role<DP, SHARED>(p, plan, &kmap, &vmap, slots, sh, c, begin, end, lane);
-            __syncwarp();
+            tile_load_role<DP>(p, plan, &kmap, &vmap, slots, sh, lane);
+        } else {
+            const int w = warp - kQueryWarp;
+            tile_query_role<DP, SHARED>(p, plan, &qmap, q + w * R::kQ, sh, c, begin, end, share, w,
+                                        lane);
         }
     }
+    __syncwarp();
     asm volatile("cp.async.wait_all;" ::: "memory");
     tc_fence_before();
     __syncthreads();
@@ -1103,6 +1344,24 @@ cudaError_t pool_map(CUtensorMap* map, const void* pool, const AttentionParams& 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The queries as [token][head][value]; a copy takes 64 values of g heads of
+// 128 / g tokens.
+cudaError_t query_map(CUtensorMap* map, const AttentionParams& p, int g)
+{
+    EncodeTiled encode = encode_tiled();
+    if (encode == nullptr)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.hq, (cuuint64_t)p.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t sizes[3] = {64, (cuuint32_t)g, (cuuint32_t)(kSubRows / g)};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q),
+                              dims, strides, sizes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int box_slots(int page_size)
 {
     int box = 8;
@@ -1113,30 +1372,37 @@ int box_slots(int page_size)
 
 template <int DP, bool FULL, bool SHARED>
 cudaError_t launch_tiles_f(const AttentionParams& p, const TilePlan& plan, const CUtensorMap& kmap,
-                           const CUtensorMap& vmap, int sm_count, cudaStream_t st)
+                           const CUtensorMap& vmap, const CUtensorMap& qmap, int sm_count,
+                           cudaStream_t st)
 {
     auto kernel = attention_tiles_kernel<DP, FULL, SHARED>;
     int ctas = 0;
-    const cudaError_t err = resident_ctas(kernel, kTileThreads, TileTraits<DP>::kSmem, &ctas);
+    constexpr int kSmem = tile_smem<DP>();
+    static_assert(kSmem <= (int)kMaxSmemPerCta, "shared memory of a CTA");
+    cudaError_t err = resident_ctas(kernel, kTileThreads, kSmem, &ctas);
     if (err != cudaSuccess)
         return err;
     if (ctas < 1)
         return cudaErrorNotSupported;
     // one CTA an SM: each takes all of its SM's tensor memory
     const int grid = std::min(sm_count, kMaxTileCtas);
-    return launch(kernel, dim3(grid), dim3(kTileThreads), TileTraits<DP>::kSmem, st, p, plan, kmap,
-                  vmap);
+    err = launch(kernel, dim3(grid), dim3(kTileThreads), kSmem, st, p, plan, kmap, vmap, qmap);
+    if (err != cudaSuccess)
+        return err;
+    return launch(attention_join_kernel<DP, SHARED>, dim3(grid, 2, DP / 32), dim3(kSubRows), 0, st,
+                  p, plan);
 }
 
 template <int DP>
 cudaError_t launch_tiles_d(const AttentionParams& p, const TilePlan& plan, const CUtensorMap& kmap,
-                           const CUtensorMap& vmap, bool full, int sm_count, cudaStream_t st)
+                           const CUtensorMap& vmap, const CUtensorMap& qmap, bool full,
+                           int sm_count, cudaStream_t st)
 {
     if (p.group_start)
-        return full ? launch_tiles_f<DP, true, true>(p, plan, kmap, vmap, sm_count, st)
-                    : launch_tiles_f<DP, false, true>(p, plan, kmap, vmap, sm_count, st);
-    return full ? launch_tiles_f<DP, true, false>(p, plan, kmap, vmap, sm_count, st)
-                : launch_tiles_f<DP, false, false>(p, plan, kmap, vmap, sm_count, st);
+        return full ? launch_tiles_f<DP, true, true>(p, plan, kmap, vmap, qmap, sm_count, st)
+                    : launch_tiles_f<DP, false, true>(p, plan, kmap, vmap, qmap, sm_count, st);
+    return full ? launch_tiles_f<DP, true, false>(p, plan, kmap, vmap, qmap, sm_count, st)
+                : launch_tiles_f<DP, false, false>(p, plan, kmap, vmap, qmap, sm_count, st);
 }
 
 }  // namespace
@@ -1152,11 +1418,11 @@ bool tiles_can_run(const AttentionParams& p, arops_dtype dtype)
 
 size_t tile_part_bytes(int dp)
 {
-    return (size_t)kMaxTileCtas * 4 * tile_part_floats(dp) * sizeof(float);
+    return (size_t)kMaxTileCtas * (4 * tile_part_floats(dp) * sizeof(float) + 32);
 }
 
-cudaError_t launch_attention_tiles(const AttentionParams& p, int32_t* counters, float* parts,
-                                   float* prefix_o, float* prefix_ml, int sm_count,
+cudaError_t launch_attention_tiles(const AttentionParams& p, float* parts, float* prefix_o,
+                                   float* prefix_ml, int sm_count,
                                    cudaStream_t stream)
 {
     TilePlan plan = {};
@@ -1166,21 +1432,27 @@ cudaError_t launch_attention_tiles(const AttentionParams& p, int32_t* counters, 
     plan.score = make_score_map(p);
     if (full)
         plan.score.scale = p.scale;
-    plan.counters = counters;
     plan.parts = parts;
+    plan.splits = reinterpret_cast<TileSplit*>(
+        parts + (size_t)kMaxTileCtas * 4 * tile_part_floats(p.head_dim <= 64 ? 64 : 128));
     plan.prefix_o = prefix_o;
     plan.prefix_ml = prefix_ml;
     plan.g = make_row_divide(p.hq / p.hk);
     plan.box = box_slots(p.map.page_size);
-    CUtensorMap kmap, vmap;
+    // whole tokens in the 128 rows of a sub-tile, and strides that a map can hold
+    const int g = p.hq / p.hk;
+    plan.q_map = kSubRows % g == 0 && p.q_stride < (1ll << 38);
+    CUtensorMap kmap, vmap, qmap = {};
     cudaError_t err = pool_map(&kmap, p.k_pages, p, plan.box);
     if (err == cudaSuccess)
         err = pool_map(&vmap, p.v_pages, p, plan.box);
+    if (err == cudaSuccess && plan.q_map)
+        err = query_map(&qmap, p, g);
     if (err != cudaSuccess)
         return err;
     return p.head_dim <= 64
-               ? launch_tiles_d<64>(p, plan, kmap, vmap, full, sm_count, stream)
-               : launch_tiles_d<128>(p, plan, kmap, vmap, full, sm_count, stream);
+               ? launch_tiles_d<64>(p, plan, kmap, vmap, qmap, full, sm_count, stream)
+               : launch_tiles_d<128>(p, plan, kmap, vmap, qmap, full, sm_count, stream);
 }
 
 }  // namespace arops

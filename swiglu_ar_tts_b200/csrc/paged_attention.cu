@@ -1203,8 +1203,7 @@ cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* 
             prefix_o = reinterpret_cast<float*>(reinterpret_cast<char*>(plan.parts) + parts);
             prefix_ml = prefix_o + (size_t)p.tokens * p.hq * dp;
         }
-        err = launch_attention_tiles(p, plan.counters, plan.parts, prefix_o, prefix_ml, di.sm_count,
-                                     stream);
+        err = launch_attention_tiles(p, plan.parts, prefix_o, prefix_ml, di.sm_count, stream);
         if (err != cudaSuccess || !p.group_start)
             return err;
         plan.prefix_o = prefix_o;

@@ -184,6 +184,16 @@ __device__ __forceinline__ void tensor_load4(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
+__device__ __forceinline__ void tensor_load3(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                             int32_t x, int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");

@@ -530,7 +530,7 @@ __device__ void tile_query_role(const AttentionParams& p, const TilePlan& plan,
 }
 
 // ---------------------------------------------------------------------------
-// Products (one warp; one thread of it issues).
+// Products (one thread).
 // ---------------------------------------------------------------------------
 template <int DP>
 __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
@@ -548,18 +548,19 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
     uint32_t used = 0;                     // slots consumed
     uint32_t qn[2] = {0, 0}, on[2] = {0, 0}, pn[2] = {0, 0};  // waits so far
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return warp_wait(bar, parity, &sh.stop, p.err);
+        return wait_for(bar, parity, &sh.stop, p.err);
     };
     // The units of all pieces form one line: under the softmax of a piece's last
     // unit the next piece's first S is multiplied.
     struct Unit {
         int32_t u, u1, a[2], b[2];
     };
-    PieceReader<DP> reader;
+    uint32_t pieces = 0;
     auto next_piece = [&](Unit& n) {
-        TilePiece t;
-        if (!reader.next(sh, t, p.err))
+        const uint32_t slot = pieces % kPieces;
+        if (!wait(&sh.piece_full[slot], (pieces / kPieces) & 1))
             return false;
+        const TilePiece& t = sh.pieces[slot];
         n.u = t.u0;
         n.u1 = t.u1;
 #pragma unroll
@@ -567,7 +568,9 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
             n.a[w] = t.a[w];
             n.b[w] = t.b[w];
         }
-        return true;
+        mbar_arrive(smem_addr(&sh.piece_empty[slot]));
+        ++pieces;
+        return n.u < n.u1;
     };
     auto slot = [&](uint32_t& s) {
         s = used % R::kSlots;
@@ -604,24 +607,18 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
                 if (!wait(&sh.p_ready[w][0], pn[w] & 1))
                     return;
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kFirstKeys / 16; ++k)
-                        tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO,
-                                  cur.u > cur.a[w] || k > 0);
-                }
-                __syncwarp();
+                for (int k = 0; k < kFirstKeys / 16; ++k)
+                    tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO,
+                              cur.u > cur.a[w] || k > 0);
                 if (!wait(&sh.p_ready[w][1], pn[w] & 1))
                     return;
                 tc_fence_after();
                 ++pn[w];
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = kFirstKeys / 16; k < kTileUnit / 16; ++k)
-                        tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO, true);
-                    tc_commit(smem_addr(&sh.o_done[w]));
-                }
-                __syncwarp();
+                for (int k = kFirstKeys / 16; k < kTileUnit / 16; ++k)
+                    tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO, true);
+                tc_commit(smem_addr(&sh.o_done[w]));
             }
             if (more && nxt.u >= nxt.a[w] && nxt.u < nxt.b[w]) {  // the next S_w = Q_w K^T
                 if (nxt.u == nxt.a[w]) {
@@ -629,26 +626,20 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
                         return;
                     tc_fence_after();
                 }
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t off = ((k / 4) * (kTileUnit * 128) + (k % 4) * 32) >> 4;
-                        tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off, kb + off, kWordS, k > 0);
-                    }
-                    tc_commit(smem_addr(&sh.s_full[w]));
-                    if (nxt.u + 1 == nxt.b[w])
-                        tc_commit(smem_addr(&sh.q_free[w]));
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t off = ((k / 4) * (kTileUnit * 128) + (k % 4) * 32) >> 4;
+                    tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off, kb + off, kWordS, k > 0);
                 }
-                __syncwarp();
+                tc_commit(smem_addr(&sh.s_full[w]));
+                if (nxt.u + 1 == nxt.b[w])
+                    tc_commit(smem_addr(&sh.q_free[w]));
             }
         }
-        if (elect_one()) {
-            if (!first)
-                tc_commit(smem_addr(&sh.empty[vs]));
-            if (more)
-                tc_commit(smem_addr(&sh.empty[ks]));
-        }
-        __syncwarp();
+        if (!first)
+            tc_commit(smem_addr(&sh.empty[vs]));
+        if (more)
+            tc_commit(smem_addr(&sh.empty[ks]));
         if (!more)
             return;
         first = false;
@@ -658,14 +649,13 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
 // ---------------------------------------------------------------------------
 // Softmax (four warps a sub-tile, a row a thread).
 // ---------------------------------------------------------------------------
-// A row's scores from its products, in base 2: cap, then bias.
+// 32 of a row's scores from its products, in base 2: cap, then bias.
 //   |s| <= cap / 2 in all rows of the warp (a cap is there for outliers): tanh
-//   by its polynomial, 6 operations a pair of keys on the fp32 pipe instead of
-//   2 exponential-unit operations a key (12,500 -> 1,000 clocks a unit of 128
-//   keys, prompt rows with a cap of 30).
+//   by its polynomial, on the fp32 pipe, instead of 2 exponential-unit
+//   operations a key.
 //   Keys not behind the query: |i - j| without the absolute value, one FMA.
-__device__ __forceinline__ void map_row(uint32_t (&s)[kTileUnit], const ScoreMap& map, float slope,
-                                        int32_t pos, int32_t key0)
+__device__ __forceinline__ void map_scores(uint32_t (&s)[32], const ScoreMap& map, float slope,
+                                           int32_t gap)
 {
     auto at = [&](int i) {
         return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
@@ -679,12 +669,12 @@ __device__ __forceinline__ void map_row(uint32_t (&s)[kTileUnit], const ScoreMap
     if (map.cap > 0.0f) {
         float big = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kTileUnit; ++i)
+        for (int i = 0; i < 32; ++i)
             big = fmaxf(big, fabsf(__uint_as_float(s[i])));
         const float in = map.scale * map.inv_cap;
         if (__all_sync(0xFFFFFFFFu, big * fabsf(in) <= 0.5f)) {
 #pragma unroll
-            for (int i = 0; i < kTileUnit; i += 2) {
+            for (int i = 0; i < 32; i += 2) {
                 const float2 x = at(i);
                 const float2 t = mul2(x, both(in));
                 const float2 y = mul2(t, t);
@@ -696,29 +686,29 @@ __device__ __forceinline__ void map_row(uint32_t (&s)[kTileUnit], const ScoreMap
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < kTileUnit; ++i)
+            for (int i = 0; i < 32; ++i)
                 s[i] = __float_as_uint(
                     soft_cap(__uint_as_float(s[i]) * map.scale, map.cap, map.inv_cap) * kLog2e);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kTileUnit; i += 2)
+        for (int i = 0; i < 32; i += 2)
             put(i, mul2(at(i), both(out)));
     }
     if (__all_sync(0xFFFFFFFFu, slope == 0.0f))
         return;
     const float bias = -slope * kLog2e;
-    const float gap = (float)(pos - key0);
-    if (__all_sync(0xFFFFFFFFu, pos - key0 >= kTileUnit - 1)) {
-        const float first = bias * gap;
+    if (__all_sync(0xFFFFFFFFu, gap >= 31)) {
+        const float first = bias * (float)gap;
 #pragma unroll
-        for (int i = 0; i < kTileUnit; i += 2)
+        for (int i = 0; i < 32; i += 2)
             put(i, add2(at(i), fma2(both(-bias), make_float2((float)i, (float)(i + 1)),
                                     both(first))));
     } else {
 #pragma unroll
-        for (int i = 0; i < kTileUnit; ++i)
-            s[i] = __float_as_uint(fmaf(bias, fabsf(gap - (float)i), __uint_as_float(s[i])));
+        for (int i = 0; i < 32; ++i)
+            s[i] = __float_as_uint(
+                fmaf(bias, fabsf((float)gap - (float)i), __uint_as_float(s[i])));
     }
 }
 
@@ -776,37 +766,49 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
             if (!wait(&sh.s_full[w], on & 1))
                 return;
             tc_fence_after();
-            uint32_t s[kTileUnit];
+            // Two passes over the row, 32 columns at a time, the next 32 on
+            // their way from tensor memory meanwhile: first the maximum (what
+            // a row does not see goes back as -inf, mapped scores as they
+            // are), then the weights.  One pass with the row in registers took
+            // 128 of them and five times the code, and its instructions
+            // drove the other warps' out of the instruction cache: the warp of
+            // the products then waited 300 clocks at every step.
+            const bool cut = __any_sync(0xFFFFFFFFu, key0 < lo || hi - key0 < kTileUnit);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t s[2][32];
+            tc_load32(s[0], s_addr);
+#pragma unroll 1
+            for (int i = 0; i < kTileUnit; i += 64) {
 #pragma unroll
-            for (int i = 0; i < kTileUnit; i += 32)
-                tc_load32(s + i, s_addr + i);
-            tc_wait_ld();
-            tc_loaded<kTileUnit>(s);
-
-            if constexpr (FULL)
-                map_row(s, plan.score, slope, pos, key0);
-            if (__any_sync(0xFFFFFFFFu, key0 < lo || hi - key0 < kTileUnit)) {
-                const int32_t first = lo - key0, last = hi - key0;
+                for (int h = 0; h < 2; ++h) {
+                    const int col = i + 32 * h;
+                    tc_wait_ld();
+                    tc_loaded<32>(s[h]);
+                    if (col + 32 < kTileUnit)
+                        tc_load32(s[h ^ 1], s_addr + col + 32);
+                    if constexpr (FULL)
+                        map_scores(s[h], plan.score, slope, pos - key0 - col);
+                    if (cut) {
+                        const int32_t first = lo - key0 - col, last = hi - key0 - col;
 #pragma unroll
-                for (int i = 0; i < kTileUnit; ++i)
-                    s[i] = i >= first && i < last ? s[i] : __float_as_uint(-INFINITY);
+                        for (int e = 0; e < 32; ++e)
+                            s[h][e] = e >= first && e < last ? s[h][e]
+                                                             : __float_as_uint(-INFINITY);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[h][e + x])),
+                                          __uint_as_float(s[h][e + 4 + x]));
+                    if (FULL || cut)
+                        tc_store32(s_addr + col, s[h]);
+                }
             }
-            float mx[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                mx[e] = __uint_as_float(s[e]);
-#pragma unroll
-            for (int i = 8; i < kTileUnit - 8; i += 16)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[i + e])),
-                                  __uint_as_float(s[i + 8 + e]));
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                mx[e] = fmaxf(mx[e], __uint_as_float(s[kTileUnit - 8 + e]));
-            const float mu = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
-                             scale;
+            if (FULL || cut)
+                tc_wait_st();
+            tc_load32(s[0], s_addr);
+            const float mu = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
 
             // scale what there is only when a maximum has grown by 2^8
             const bool grown = mu > m + 8.0f || (m == -INFINITY && mu > -INFINITY);
@@ -837,25 +839,35 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             // the weights are rounded to bf16 (2^-8 of each at most), the type
             // of the values that they multiply; l keeps them in fp32
+#pragma unroll 1
+            for (int i = 0; i < kTileUnit; i += 64) {
 #pragma unroll
-            for (int i = 0; i < kTileUnit; i += 32) {
-                uint32_t pk[16];
+                for (int h = 0; h < 2; ++h) {
+                    const int col = i + 32 * h;
+                    tc_wait_ld();
+                    tc_loaded<32>(s[h]);
+                    // (P's columns lie in front of the scores still to be read)
+                    if (col + 32 < kTileUnit)
+                        tc_load32(s[h ^ 1], s_addr + col + 32);
+                    uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float2 x = make_float2(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1]));
-                    x = fma2(x, sc, bs);
-                    x.x = exp2_fast(x.x);
-                    x.y = exp2_fast(x.y);
-                    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
-                    pk[e >> 1] = pack_bf16x2(x.x, x.y);
-                }
-                tc_store16(s_addr + i / 2, pk);
-                if (i + 32 == kFirstKeys || i + 32 == kTileUnit) {
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(&sh.p_ready[w][i + 32 == kTileUnit]));
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 x = make_float2(__uint_as_float(s[h][e]),
+                                               __uint_as_float(s[h][e + 1]));
+                        x = fma2(x, sc, bs);
+                        x.x = exp2_fast(x.x);
+                        x.y = exp2_fast(x.y);
+                        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
+                        pk[e >> 1] = pack_bf16x2(x.x, x.y);
+                    }
+                    tc_store16(s_addr + col / 2, pk);
+                    if (col + 32 >= kFirstKeys) {
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&sh.p_ready[w][col + 32 == kTileUnit]));
+                    }
                 }
             }
             ++on;
@@ -1269,23 +1281,18 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     tc_fence_after();
     const TileCursor c = sh.found;
 
-    // Registers: the softmax warps keep a row of 128 scores, the others little.
-    // 256 x 192 + 128 x 56 + 128 x 72 = 512 x 128, what the launch gave out.
     if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         tile_softmax_role<DP, FULL, SHARED>(p, plan, sh, warp >> 2, threadIdx.x & 127);
     } else if (warp >= kResultWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         tile_result_role<DP, SHARED>(p, plan, stage, sh, threadIdx.x & 127);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kMmaWarp) {
-            tile_mma_role<DP>(p, q, slots, sh);
-            // every product and every arrival asked for has happened
-            if (elect_one())
+            if (elect_one()) {
+                tile_mma_role<DP>(p, q, slots, sh);
+                // every product and every arrival asked for has happened
                 tc_commit(smem_addr(&sh.drain));
-            __syncwarp();
-            mbar_wait(smem_addr(&sh.drain), 0);
+                mbar_wait(smem_addr(&sh.drain), 0);
+            }
         } else if (warp == kLoadWarp) {
             tile_load_role<DP>(p, plan, &kmap, &vmap, slots, sh, lane);
         } else {

@@ -35,9 +35,10 @@ constexpr int kTileRows = 2 * kSubRows;
 constexpr int kTileUnit = 128;  // keys
 constexpr int kTileThreads = 512;
 constexpr int kTileWarps = kTileThreads / 32;
-// Keys whose weights are handed to the products first, the rest follow: the
-// products of the first run under the exponentials of the rest.
-constexpr int kFirstKeys = 96;
+// A unit's scores are made and used in two halves of 64 keys, each in its own
+// columns: while one half is in the softmax, the other's weights are multiplied
+// and its next scores made.
+constexpr int kHalfUnit = kTileUnit / 2;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
 constexpr int kQueryWarp = 10;   // and 11
@@ -244,9 +245,9 @@ struct TileShared {
     uint64_t tail;        // a copy of values that reaches past the sequence's end
     uint64_t q_ready[2];
     uint64_t q_free[2];   // a piece's last product with Q_w is done
-    uint64_t s_full[2];
+    uint64_t s_full[2][2];   // [sub-tile][half]
     uint64_t p_ready[2][2];
-    uint64_t o_done[2];
+    uint64_t o_done[2][2];
     uint64_t ml_ready[2]; // a piece's m and l are in shared memory
     uint64_t o_free[2];   // a piece's O_w, m and l have been read
     uint64_t drain;
@@ -537,7 +538,7 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
                               const unsigned char* slots, TileShared<DP>& sh)
 {
     using R = TileTraits<DP>;
-    constexpr uint32_t kWordS = mma_word(kSubRows, kTileUnit, false);
+    constexpr uint32_t kWordS = mma_word(kSubRows, kHalfUnit, false);
     constexpr uint32_t kWordO = mma_word(kSubRows, DP, true);
     const uint32_t tmem = sh.tmem;
     // keys and queries: K (head_dim) contiguous, one 64-value block behind the
@@ -597,31 +598,26 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
         const uint32_t vb = v_low + vs * (R::kSlot >> 4);
         const uint32_t kb = k_low + ks * (R::kSlot >> 4);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+        for (int hw = 0; hw < 4; ++hw) {
+            const int h = hw >> 1, w = hw & 1;
             const uint32_t o = tmem + R::kO + w * DP;
-            const uint32_t s = tmem + R::kS + w * kTileUnit;
+            const uint32_t s = tmem + R::kS + w * kTileUnit + h * kHalfUnit;
             if (!first && cur.u >= cur.a[w] && cur.u < cur.b[w]) {  // O_w (+)= P_w V
                 // the piece before this one's O_w has been read
-                if (cur.u == cur.a[w] && !wait(&sh.o_free[w], (on[w]++ & 1) ^ 1))
+                if (h == 0 && cur.u == cur.a[w] && !wait(&sh.o_free[w], (on[w]++ & 1) ^ 1))
                     return;
-                if (!wait(&sh.p_ready[w][0], pn[w] & 1))
+                if (!wait(&sh.p_ready[w][h], pn[w] & 1))
                     return;
+                pn[w] += h;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kFirstKeys / 16; ++k)
-                    tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO,
-                              cur.u > cur.a[w] || k > 0);
-                if (!wait(&sh.p_ready[w][1], pn[w] & 1))
-                    return;
-                tc_fence_after();
-                ++pn[w];
-#pragma unroll
-                for (int k = kFirstKeys / 16; k < kTileUnit / 16; ++k)
-                    tc_mma_ts(o, s + k * 8, vb + k * (2048 >> 4), kWordO, true);
-                tc_commit(smem_addr(&sh.o_done[w]));
+                for (int k = 0; k < kHalfUnit / 16; ++k)
+                    tc_mma_ts(o, s + k * 8, vb + (h * (kHalfUnit / 16) + k) * (2048 >> 4), kWordO,
+                              cur.u > cur.a[w] || h > 0 || k > 0);
+                tc_commit(smem_addr(&sh.o_done[w][h]));
             }
             if (more && nxt.u >= nxt.a[w] && nxt.u < nxt.b[w]) {  // the next S_w = Q_w K^T
-                if (nxt.u == nxt.a[w]) {
+                if (h == 0 && nxt.u == nxt.a[w]) {
                     if (!wait(&sh.q_ready[w], qn[w]++ & 1))
                         return;
                     tc_fence_after();
@@ -629,10 +625,11 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     const uint32_t off = ((k / 4) * (kTileUnit * 128) + (k % 4) * 32) >> 4;
-                    tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off, kb + off, kWordS, k > 0);
+                    tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off,
+                              kb + (h * kHalfUnit * 128 >> 4) + off, kWordS, k > 0);
                 }
-                tc_commit(smem_addr(&sh.s_full[w]));
-                if (nxt.u + 1 == nxt.b[w])
+                tc_commit(smem_addr(&sh.s_full[w][h]));
+                if (h == 1 && nxt.u + 1 == nxt.b[w])
                     tc_commit(smem_addr(&sh.q_free[w]));
             }
         }
@@ -649,12 +646,12 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
 // ---------------------------------------------------------------------------
 // Softmax (four warps a sub-tile, a row a thread).
 // ---------------------------------------------------------------------------
-// 32 of a row's scores from its products, in base 2: cap, then bias.
+// Half a unit of a row's scores from its products, in base 2: cap, then bias.
 //   |s| <= cap / 2 in all rows of the warp (a cap is there for outliers): tanh
 //   by its polynomial, on the fp32 pipe, instead of 2 exponential-unit
 //   operations a key.
 //   Keys not behind the query: |i - j| without the absolute value, one FMA.
-__device__ __forceinline__ void map_scores(uint32_t (&s)[32], const ScoreMap& map, float slope,
+__device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const ScoreMap& map, float slope,
                                            int32_t gap)
 {
     auto at = [&](int i) {
@@ -669,12 +666,12 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[32], const ScoreMap& ma
     if (map.cap > 0.0f) {
         float big = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < kHalfUnit; ++i)
             big = fmaxf(big, fabsf(__uint_as_float(s[i])));
         const float in = map.scale * map.inv_cap;
         if (__all_sync(0xFFFFFFFFu, big * fabsf(in) <= 0.5f)) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < kHalfUnit; i += 2) {
                 const float2 x = at(i);
                 const float2 t = mul2(x, both(in));
                 const float2 y = mul2(t, t);
@@ -686,27 +683,27 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[32], const ScoreMap& ma
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < kHalfUnit; ++i)
                 s[i] = __float_as_uint(
                     soft_cap(__uint_as_float(s[i]) * map.scale, map.cap, map.inv_cap) * kLog2e);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2)
+        for (int i = 0; i < kHalfUnit; i += 2)
             put(i, mul2(at(i), both(out)));
     }
     if (__all_sync(0xFFFFFFFFu, slope == 0.0f))
         return;
     const float bias = -slope * kLog2e;
-    if (__all_sync(0xFFFFFFFFu, gap >= 31)) {
+    if (__all_sync(0xFFFFFFFFu, gap >= kHalfUnit - 1)) {
         const float first = bias * (float)gap;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2)
+        for (int i = 0; i < kHalfUnit; i += 2)
             put(i, add2(at(i), fma2(both(-bias), make_float2((float)i, (float)(i + 1)),
                                     both(first))));
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < kHalfUnit; ++i)
             s[i] = __float_as_uint(
                 fmaf(bias, fabsf((float)gap - (float)i), __uint_as_float(s[i])));
     }
@@ -719,7 +716,7 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
     using R = TileTraits<DP>;
     const int lane = tid & 31;
     const uint32_t lanes = (uint32_t)(tid & ~31) << 16;  // the warp's lanes of tensor memory
-    const uint32_t s_addr = sh.tmem + lanes + R::kS + w * kTileUnit;
+    const uint32_t s_base = sh.tmem + lanes + R::kS + w * kTileUnit;
     const uint32_t o_addr = sh.tmem + lanes + R::kO + w * DP;
     uint32_t on = 0;     // units done: S tiles seen, P V products asked for
     uint32_t ended = 0;  // pieces with units of this sub-tile
@@ -762,117 +759,87 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
             continue;
         key0 += a * kTileUnit;
         float m = -INFINITY, l = 0.0f;
-        for (int32_t n = b - a; n > 0; --n, key0 += kTileUnit) {
-            if (!wait(&sh.s_full[w], on & 1))
-                return;
-            tc_fence_after();
-            // Two passes over the row, 32 columns at a time, the next 32 on
-            // their way from tensor memory meanwhile: first the maximum (what
-            // a row does not see goes back as -inf, mapped scores as they
-            // are), then the weights.  One pass with the row in registers took
-            // 128 of them and five times the code, and its instructions
-            // drove the other warps' out of the instruction cache: the warp of
-            // the products then waited 300 clocks at every step.
-            const bool cut = __any_sync(0xFFFFFFFFu, key0 < lo || hi - key0 < kTileUnit);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            uint32_t s[2][32];
-            tc_load32(s[0], s_addr);
+        for (int32_t n = b - a; n > 0; --n) {
 #pragma unroll 1
-            for (int i = 0; i < kTileUnit; i += 64) {
+            for (int h = 0; h < 2; ++h, key0 += kHalfUnit) {
+                if (!wait(&sh.s_full[w][h], on & 1))
+                    return;
+                tc_fence_after();
+                const uint32_t s_addr = s_base + h * kHalfUnit;
+                uint32_t s[kHalfUnit];
+                tc_load32(s, s_addr);
+                tc_load32(s + 32, s_addr + 32);
+                tc_wait_ld();
+                tc_loaded<kHalfUnit>(s);
+                if constexpr (FULL)
+                    map_scores(s, plan.score, slope, pos - key0);
+                if (__any_sync(0xFFFFFFFFu, key0 < lo || hi - key0 < kHalfUnit)) {
+                    const int32_t first = lo - key0, last = hi - key0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int col = i + 32 * h;
-                    tc_wait_ld();
-                    tc_loaded<32>(s[h]);
-                    if (col + 32 < kTileUnit)
-                        tc_load32(s[h ^ 1], s_addr + col + 32);
-                    if constexpr (FULL)
-                        map_scores(s[h], plan.score, slope, pos - key0 - col);
-                    if (cut) {
-                        const int32_t first = lo - key0 - col, last = hi - key0 - col;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            s[h][e] = e >= first && e < last ? s[h][e]
-                                                             : __float_as_uint(-INFINITY);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[h][e + x])),
-                                          __uint_as_float(s[h][e + 4 + x]));
-                    if (FULL || cut)
-                        tc_store32(s_addr + col, s[h]);
+                    for (int e = 0; e < kHalfUnit; ++e)
+                        s[e] = e >= first && e < last ? s[e] : __float_as_uint(-INFINITY);
                 }
-            }
-            if (FULL || cut)
-                tc_wait_st();
-            tc_load32(s[0], s_addr);
-            const float mu = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                float mx[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mx[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[4 + x]));
+#pragma unroll
+                for (int e = 8; e < kHalfUnit; e += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(s[e + x])),
+                                      __uint_as_float(s[e + 4 + x]));
+                const float mu = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
 
-            // scale what there is only when a maximum has grown by 2^8
-            const bool grown = mu > m + 8.0f || (m == -INFINITY && mu > -INFINITY);
-            if (__any_sync(0xFFFFFFFFu, grown)) {
-                const float mn = fmaxf(m, mu);
-                const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
-                m = mn;
-                l *= f;
-                if (n < b - a) {
-                    if (!wait(&sh.o_done[w], (on - 1) & 1))
-                        return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < DP; i += 16) {
-                        uint32_t o[16];
-                        tc_load16(o, o_addr + i);
-                        tc_wait_ld();
-                        tc_loaded<16>(o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc_store16(o_addr + i, o);
-                    }
-                }
-            }
-            const float base = m == -INFINITY ? 0.0f : -m;
-            const float2 sc = make_float2(scale, scale), bs = make_float2(base, base);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            // the weights are rounded to bf16 (2^-8 of each at most), the type
-            // of the values that they multiply; l keeps them in fp32
+                // scale what there is only when a maximum has grown by 2^8
+                const bool grown = mu > m + 8.0f || (m == -INFINITY && mu > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, grown)) {
+                    const float mn = fmaxf(m, mu);
+                    const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (h > 0 || n < b - a) {
+                        if (!wait(&sh.o_done[w][h ^ 1], h > 0 ? on & 1 : (on - 1) & 1))
+                            return;
+                        tc_fence_after();
 #pragma unroll 1
-            for (int i = 0; i < kTileUnit; i += 64) {
+                        for (int i = 0; i < DP; i += 16) {
+                            uint32_t o[16];
+                            tc_load16(o, o_addr + i);
+                            tc_wait_ld();
+                            tc_loaded<16>(o);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int col = i + 32 * h;
-                    tc_wait_ld();
-                    tc_loaded<32>(s[h]);
-                    // (P's columns lie in front of the scores still to be read)
-                    if (col + 32 < kTileUnit)
-                        tc_load32(s[h ^ 1], s_addr + col + 32);
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 x = make_float2(__uint_as_float(s[h][e]),
-                                               __uint_as_float(s[h][e + 1]));
-                        x = fma2(x, sc, bs);
-                        x.x = exp2_fast(x.x);
-                        x.y = exp2_fast(x.y);
-                        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
-                        pk[e >> 1] = pack_bf16x2(x.x, x.y);
-                    }
-                    tc_store16(s_addr + col / 2, pk);
-                    if (col + 32 >= kFirstKeys) {
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(smem_addr(&sh.p_ready[w][col + 32 == kTileUnit]));
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_store16(o_addr + i, o);
+                        }
                     }
                 }
+                const float base = m == -INFINITY ? 0.0f : -m;
+                const float2 sc = make_float2(scale, scale), bs = make_float2(base, base);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                // the weights are rounded to bf16 (2^-8 of each at most), the
+                // type of the values that they multiply; l keeps them in fp32
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < kHalfUnit; e += 2) {
+                    float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    x = fma2(x, sc, bs);
+                    x.x = exp2_fast(x.x);
+                    x.y = exp2_fast(x.y);
+                    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
+                    pk[e >> 1] = pack_bf16x2(x.x, x.y);
+                }
+                tc_store32(s_addr, pk);
+                const float2 all = add2(sum[0], sum[1]);
+                l += all.x + all.y;
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.p_ready[w][h]));
             }
             ++on;
-            const float2 all = add2(sum[0], sum[1]);
-            l += all.x + all.y;
         }
         if (!wait(&sh.o_free[w], (ended & 1) ^ 1))
             return;
@@ -969,7 +936,7 @@ __device__ void tile_result_role(const AttentionParams& p, const TilePlan& plan,
                     ++ended0;
                 }
                 const bool ok = warp_wait(&sh.ml_ready[w], piece & 1, &sh.stop, p.err) &&
-                                warp_wait(&sh.o_done[w], done & 1, &sh.stop, p.err);
+                                warp_wait(&sh.o_done[w][1], done & 1, &sh.stop, p.err);
                 if (!result_agree(ok))
                     return;
                 tc_fence_after();
@@ -1150,10 +1117,11 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_addr(&sh.q_ready[w]), 1);
             mbar_init(smem_addr(&sh.q_free[w]), 1);
-            mbar_init(smem_addr(&sh.s_full[w]), 1);
-            mbar_init(smem_addr(&sh.p_ready[w][0]), 4);
-            mbar_init(smem_addr(&sh.p_ready[w][1]), 4);
-            mbar_init(smem_addr(&sh.o_done[w]), 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(smem_addr(&sh.s_full[w][h]), 1);
+                mbar_init(smem_addr(&sh.p_ready[w][h]), 4);
+                mbar_init(smem_addr(&sh.o_done[w][h]), 1);
+            }
             mbar_init(smem_addr(&sh.ml_ready[w]), 4);
             mbar_init(smem_addr(&sh.o_free[w]), 4);
         }

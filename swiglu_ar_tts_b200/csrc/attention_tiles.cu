@@ -41,7 +41,7 @@ constexpr int kTileWarps = kTileThreads / 32;
 constexpr int kHalfUnit = kTileUnit / 2;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
-constexpr int kQueryWarp = 10;   // and 11
+constexpr int kMmaWarp1 = 11;    // of sub-tile 1; warp 10 makes pieces
 constexpr int kResultWarp = 12;  // to 15
 
 // Largest grid: the workspace holds four partial results a CTA.
@@ -250,7 +250,7 @@ struct TileShared {
     uint64_t o_done[2][2];
     uint64_t ml_ready[2]; // a piece's m and l are in shared memory
     uint64_t o_free[2];   // a piece's O_w, m and l have been read
-    uint64_t drain;
+    uint64_t drain[2];
     TilePiece pieces[kPieces];
     float m[2][kSubRows], l[2][kSubRows];
     uint32_t tmem;
@@ -271,11 +271,8 @@ constexpr int tile_smem()
 }
 
 // Waits for `parity` of `bar`; false once anybody's wait has run out.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* stop, unsigned* err)
+__device__ __noinline__ bool wait_slow(uint32_t b, uint32_t parity, int* stop, unsigned* err)
 {
-    const uint32_t b = smem_addr(bar);
-    if (mbar_try_wait(b, parity))
-        return true;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
         for (int i = 0; i < 16; ++i)
@@ -289,6 +286,12 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* st
             return false;
         }
     }
+}
+
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* stop, unsigned* err)
+{
+    const uint32_t b = smem_addr(bar);
+    return mbar_try_wait(b, parity) || wait_slow(b, parity, stop, err);
 }
 
 // A warp's wait: all lanes go on together, or none does.
@@ -394,7 +397,7 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
 }
 
 // ---------------------------------------------------------------------------
-// Queries (one warp a sub-tile; sub-tile 0's also makes the pieces).
+// Pieces and queries (one warp).
 // ---------------------------------------------------------------------------
 // (token, head) of rows that a thread takes `step` apart.
 struct RowStep {
@@ -471,26 +474,10 @@ template <int DP, bool SHARED>
 __device__ void tile_query_role(const AttentionParams& p, const TilePlan& plan,
                                 const CUtensorMap* qmap, unsigned char* q, TileShared<DP>& sh,
                                 const TileCursor& from, int64_t begin, int64_t end, int64_t share,
-                                int w, int lane)
+                                int lane)
 {
-    uint32_t loaded = 0;
-    auto load = [&](const TilePiece& t) {
-        if (w ? t.a[1] >= t.b[1] : t.a[0] >= t.b[0])
-            return true;
-        if (!warp_wait(&sh.q_free[w], (loaded & 1) ^ 1, &sh.stop, p.err))
-            return false;
-        ++loaded;
-        load_queries<DP>(p, plan, qmap, t, w, q, &sh.q_ready[w], lane);
-        return true;
-    };
+    uint32_t phase = 3;  // parity of the next wait for q_free, a bit a sub-tile
     TilePiece t;
-    if (w == 1) {
-        PieceReader<DP> reader;
-        while (reader.next(sh, t, p.err))
-            if (!load(t))
-                return;
-        return;
-    }
     TileWalk walk(from, begin, end);
     bool more = true;
     for (uint32_t n = 0; more; ++n) {
@@ -525,36 +512,47 @@ __device__ void tile_query_role(const AttentionParams& p, const TilePlan& plan,
             mbar_arrive(smem_addr(&sh.piece_full[slot]));
         }
         __syncwarp();
-        if (more && !load(t))
+        if (!more)
             return;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if (t.a[w] >= t.b[w])
+                continue;
+            if (!warp_wait(&sh.q_free[w], (phase >> w) & 1, &sh.stop, p.err))
+                return;
+            phase ^= 1u << w;
+            load_queries<DP>(p, plan, qmap, t, w, q + w * TileTraits<DP>::kQ, &sh.q_ready[w],
+                             lane);
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Products (one thread).
+// Products (one thread of one warp a sub-tile).
 // ---------------------------------------------------------------------------
 template <int DP>
 __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
-                              const unsigned char* slots, TileShared<DP>& sh)
+                              const unsigned char* slots, TileShared<DP>& sh, int w)
 {
     using R = TileTraits<DP>;
     constexpr uint32_t kWordS = mma_word(kSubRows, kHalfUnit, false);
     constexpr uint32_t kWordO = mma_word(kSubRows, DP, true);
-    const uint32_t tmem = sh.tmem;
     // keys and queries: K (head_dim) contiguous, one 64-value block behind the
     // other; values: N (head_dim) contiguous, the leading offset between blocks
     const uint32_t q_low = operand_low(smem_addr(q), 16);
     const uint32_t k_low = operand_low(smem_addr(slots), 16);
     const uint32_t v_low = operand_low(smem_addr(slots), kTileUnit * 128);
-    uint32_t used = 0;                     // slots consumed
-    uint32_t qn[2] = {0, 0}, on[2] = {0, 0}, pn[2] = {0, 0};  // waits so far
+    const uint32_t o = sh.tmem + R::kO + w * DP;
+    const uint32_t s = sh.tmem + R::kS + w * kTileUnit;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return wait_for(bar, parity, &sh.stop, p.err);
     };
     // The units of all pieces form one line: under the softmax of a piece's last
-    // unit the next piece's first S is multiplied.
+    // unit the next piece's first S is multiplied.  Each sub-tile has a warp:
+    // one for both needed 4,000 clocks a unit for its ~600 instructions between
+    // those of the softmax, the tensor cores 2,600.
     struct Unit {
-        int32_t u, u1, a[2], b[2];
+        int32_t u, u1, a, b;
     };
     uint32_t pieces = 0;
     auto next_piece = [&](Unit& n) {
@@ -562,84 +560,79 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
         if (!wait(&sh.piece_full[slot], (pieces / kPieces) & 1))
             return false;
         const TilePiece& t = sh.pieces[slot];
-        n.u = t.u0;
-        n.u1 = t.u1;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            n.a[w] = t.a[w];
-            n.b[w] = t.b[w];
-        }
+        n = {t.u0, t.u1, t.a[w], t.b[w]};
         mbar_arrive(smem_addr(&sh.piece_empty[slot]));
         ++pieces;
         return n.u < n.u1;
     };
-    auto slot = [&](uint32_t& s) {
-        s = used % R::kSlots;
-        const bool ok = wait(&sh.full[s], (used / R::kSlots) & 1);
-        ++used;
-        return ok;
-    };
-    Unit cur, nxt;
-    bool first = true, more = next_piece(nxt);
-    while (first ? more : true) {
-        // slots in order: keys 0, values 0, keys 1, values 1, ...
+    uint32_t used = 0;  // slots consumed: keys 0, values 0, keys 1, values 1, ...
+    uint32_t p_phase = 0, q_phase = 0, o_phase = 1;  // parity of the next wait
+    Unit cur = {0, 0, 0, 0}, nxt;
+    bool have = false, more = next_piece(nxt);
+    while (have || more) {
         uint32_t vs = 0, ks = 0;
-        if (!first) {
-            cur = nxt;
-            if (nxt.u + 1 < nxt.u1)
-                ++nxt.u;
-            else
-                more = next_piece(nxt);
-            if (!slot(vs))
+        if (have) {
+            vs = used % R::kSlots;
+            if (!wait(&sh.full[vs], (used / R::kSlots) & 1))
                 return;
+            ++used;
         }
-        if (more && !slot(ks))
-            return;
+        if (more) {
+            ks = used % R::kSlots;
+            if (!wait(&sh.full[ks], (used / R::kSlots) & 1))
+                return;
+            ++used;
+        }
         const uint32_t vb = v_low + vs * (R::kSlot >> 4);
         const uint32_t kb = k_low + ks * (R::kSlot >> 4);
+        const bool pv = have && cur.u >= cur.a && cur.u < cur.b;
+        const bool qk = more && nxt.u >= nxt.a && nxt.u < nxt.b;
+        if (pv && cur.u == cur.a) {  // the piece before this one's O_w has been read
+            if (!wait(&sh.o_free[w], o_phase))
+                return;
+            o_phase ^= 1;
+        }
 #pragma unroll
-        for (int hw = 0; hw < 4; ++hw) {
-            const int h = hw >> 1, w = hw & 1;
-            const uint32_t o = tmem + R::kO + w * DP;
-            const uint32_t s = tmem + R::kS + w * kTileUnit + h * kHalfUnit;
-            if (!first && cur.u >= cur.a[w] && cur.u < cur.b[w]) {  // O_w (+)= P_w V
-                // the piece before this one's O_w has been read
-                if (h == 0 && cur.u == cur.a[w] && !wait(&sh.o_free[w], (on[w]++ & 1) ^ 1))
+        for (int h = 0; h < 2; ++h) {
+            if (pv) {  // O_w (+)= P_w V
+                if (!wait(&sh.p_ready[w][h], p_phase))
                     return;
-                if (!wait(&sh.p_ready[w][h], pn[w] & 1))
-                    return;
-                pn[w] += h;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < kHalfUnit / 16; ++k)
-                    tc_mma_ts(o, s + k * 8, vb + (h * (kHalfUnit / 16) + k) * (2048 >> 4), kWordO,
-                              cur.u > cur.a[w] || h > 0 || k > 0);
+                    tc_mma_ts(o, s + h * kHalfUnit + k * 8,
+                              vb + (h * (kHalfUnit / 16) + k) * (2048 >> 4), kWordO,
+                              h > 0 || k > 0 || cur.u > cur.a);
                 tc_commit(smem_addr(&sh.o_done[w][h]));
             }
-            if (more && nxt.u >= nxt.a[w] && nxt.u < nxt.b[w]) {  // the next S_w = Q_w K^T
-                if (h == 0 && nxt.u == nxt.a[w]) {
-                    if (!wait(&sh.q_ready[w], qn[w]++ & 1))
+            if (qk) {  // the next S_w = Q_w K^T
+                if (h == 0 && nxt.u == nxt.a) {
+                    if (!wait(&sh.q_ready[w], q_phase))
                         return;
+                    q_phase ^= 1;
                     tc_fence_after();
                 }
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     const uint32_t off = ((k / 4) * (kTileUnit * 128) + (k % 4) * 32) >> 4;
-                    tc_mma_ss(s, q_low + w * (R::kQ >> 4) + off,
+                    tc_mma_ss(s + h * kHalfUnit, q_low + off,
                               kb + (h * kHalfUnit * 128 >> 4) + off, kWordS, k > 0);
                 }
                 tc_commit(smem_addr(&sh.s_full[w][h]));
-                if (h == 1 && nxt.u + 1 == nxt.b[w])
-                    tc_commit(smem_addr(&sh.q_free[w]));
             }
         }
-        if (!first)
+        if (pv)
+            p_phase ^= 1;
+        if (qk && nxt.u + 1 == nxt.b)
+            tc_commit(smem_addr(&sh.q_free[w]));
+        if (have)
             tc_commit(smem_addr(&sh.empty[vs]));
         if (more)
             tc_commit(smem_addr(&sh.empty[ks]));
-        if (!more)
-            return;
-        first = false;
+        have = more;
+        cur = nxt;
+        if (more && ++nxt.u >= nxt.u1)
+            more = next_piece(nxt);
     }
 }
 
@@ -1104,16 +1097,16 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     if (threadIdx.x == 0) {
         for (int i = 0; i < R::kSlots; ++i) {
             mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), 2);  // both sub-tiles' products
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_addr(&sh.piece_full[i]), 1);
-            // read by the warps of copies, products, softmax, results and the
-            // second one of queries
-            mbar_init(smem_addr(&sh.piece_empty[i]), 1 + 1 + 8 + 4 + 1);
+            // read by the warps of copies, products, softmax and results
+            mbar_init(smem_addr(&sh.piece_empty[i]), 1 + 2 + 8 + 4);
         }
         mbar_init(smem_addr(&sh.tail), 1);
-        mbar_init(smem_addr(&sh.drain), 1);
+        mbar_init(smem_addr(&sh.drain[0]), 1);
+        mbar_init(smem_addr(&sh.drain[1]), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_addr(&sh.q_ready[w]), 1);
             mbar_init(smem_addr(&sh.q_free[w]), 1);
@@ -1254,19 +1247,18 @@ attention_tiles_kernel(const __grid_constant__ AttentionParams p,
     } else if (warp >= kResultWarp) {
         tile_result_role<DP, SHARED>(p, plan, stage, sh, threadIdx.x & 127);
     } else {
-        if (warp == kMmaWarp) {
+        if (warp == kMmaWarp || warp == kMmaWarp1) {
+            const int w = warp == kMmaWarp1;
             if (elect_one()) {
-                tile_mma_role<DP>(p, q, slots, sh);
+                tile_mma_role<DP>(p, q + w * R::kQ, slots, sh, w);
                 // every product and every arrival asked for has happened
-                tc_commit(smem_addr(&sh.drain));
-                mbar_wait(smem_addr(&sh.drain), 0);
+                tc_commit(smem_addr(&sh.drain[w]));
+                mbar_wait(smem_addr(&sh.drain[w]), 0);
             }
         } else if (warp == kLoadWarp) {
             tile_load_role<DP>(p, plan, &kmap, &vmap, slots, sh, lane);
         } else {
-            const int w = warp - kQueryWarp;
-            tile_query_role<DP, SHARED>(p, plan, &qmap, q + w * R::kQ, sh, c, begin, end, share, w,
-                                        lane);
+            tile_query_role<DP, SHARED>(p, plan, &qmap, q, sh, c, begin, end, share, lane);
         }
     }
     __syncwarp();

@@ -36,10 +36,11 @@ __device__ __forceinline__ float soft_cap(float s, float cap, float inv_cap)
     return cap - 2.0f * cap * reciprocal_fast(1.0f + e);
 }
 
-// tanh(x) = x P(x^2) for |x| <= 1/2, P of degree 4 with the least largest error
-// (1.3e-8 of tanh; Lawson's iteration on Chebyshev nodes).
-constexpr float kTanh0 = 1.0f, kTanh1 = -0.33333075f, kTanh2 = 0.13324907f,
-                kTanh3 = -0.052994233f, kTanh4 = 0.017151300f;
+// tanh(x) = x P(x^2) for |x| <= 1/2, P of degree 3 with the least largest
+// relative error (5.4e-7; Lawson's iteration on Chebyshev nodes).  That is 2^-21
+// of the cap at most, the size of the other roundings of a score.
+constexpr float kTanh0 = 0.99999946f, kTanh1 = -0.33326319f, kTanh2 = 0.13190296f,
+                kTanh3 = -0.044402227f;
 
 // What a kernel does to a raw product q.k, in base 2: with neither cap nor
 // slopes only scale * log2(e).

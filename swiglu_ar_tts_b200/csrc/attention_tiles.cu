@@ -642,10 +642,10 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
 // Half a unit of a row's scores from its products, in base 2: cap, then bias.
 //   |s| <= cap / 2 in all rows of the warp (a cap is there for outliers): tanh
 //   by its polynomial, on the fp32 pipe, instead of 2 exponential-unit
-//   operations a key.
+//   operations a key; scale and base are in its coefficients.
 //   Keys not behind the query: |i - j| without the absolute value, one FMA.
-__device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const ScoreMap& map, float slope,
-                                           int32_t gap)
+__device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const ScoreMap& map,
+                                           float slope, int32_t gap)
 {
     auto at = [&](int i) {
         return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
@@ -656,24 +656,34 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const Score
     };
     auto both = [](float x) { return make_float2(x, x); };
     const float out = map.scale * kLog2e;
+    const float bias = -slope * kLog2e;
+    const float2 step = both(-bias), first = both(bias * (float)gap);
+    const bool behind = __any_sync(0xFFFFFFFFu, gap < kHalfUnit - 1);
     if (map.cap > 0.0f) {
         float big = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kHalfUnit; ++i)
-            big = fmaxf(big, fabsf(__uint_as_float(s[i])));
-        const float in = map.scale * map.inv_cap;
+        for (int i = 0; i < kHalfUnit; i += 2)
+            big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[i]))),
+                        fabsf(__uint_as_float(s[i + 1])));
+        const float in = map.scale * map.inv_cap, in2 = in * in;
         if (__all_sync(0xFFFFFFFFu, big * fabsf(in) <= 0.5f)) {
+            const float2 c0 = both(kTanh0 * out), c1 = both(kTanh1 * out * in2),
+                         c2 = both(kTanh2 * out * (in2 * in2)),
+                         c3 = both(kTanh3 * out * (in2 * in2 * in2));
 #pragma unroll
             for (int i = 0; i < kHalfUnit; i += 2) {
                 const float2 x = at(i);
-                const float2 t = mul2(x, both(in));
-                const float2 y = mul2(t, t);
-                float2 q = fma2(y, both(kTanh4), both(kTanh3));
-                q = fma2(q, y, both(kTanh2));
-                q = fma2(q, y, both(kTanh1));
-                q = fma2(q, y, both(kTanh0));
-                put(i, mul2(mul2(x, both(out)), q));
+                const float2 y = mul2(x, x);
+                float2 q = fma2(y, c3, c2);
+                q = fma2(q, y, c1);
+                q = fma2(q, y, c0);
+                if (behind)
+                    put(i, mul2(x, q));
+                else
+                    put(i, fma2(x, q, fma2(step, make_float2((float)i, (float)(i + 1)), first)));
             }
+            if (!behind)
+                return;
         } else {
 #pragma unroll
             for (int i = 0; i < kHalfUnit; ++i)
@@ -687,19 +697,9 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const Score
     }
     if (__all_sync(0xFFFFFFFFu, slope == 0.0f))
         return;
-    const float bias = -slope * kLog2e;
-    if (__all_sync(0xFFFFFFFFu, gap >= kHalfUnit - 1)) {
-        const float first = bias * (float)gap;
 #pragma unroll
-        for (int i = 0; i < kHalfUnit; i += 2)
-            put(i, add2(at(i), fma2(both(-bias), make_float2((float)i, (float)(i + 1)),
-                                    both(first))));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kHalfUnit; ++i)
-            s[i] = __float_as_uint(
-                fmaf(bias, fabsf((float)gap - (float)i), __uint_as_float(s[i])));
-    }
+    for (int i = 0; i < kHalfUnit; ++i)
+        s[i] = __float_as_uint(fmaf(bias, fabsf((float)gap - (float)i), __uint_as_float(s[i])));
 }
 
 template <int DP, bool FULL, bool SHARED>

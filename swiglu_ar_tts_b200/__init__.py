@@ -324,6 +324,55 @@ def mrope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torc
     return q_out
 
 
+# The paged-cache calls are made a few times a layer with a dozen tensors each:
+# their checks are one pass of cheap comparisons, and only a failed one looks
+# for the words to say what is wrong.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch(device: int, fn, *args) -> None:
+    """fn(*args, the device's current stream), with `device` current."""
+    if torch.cuda.current_device() == device:
+        status = fn(*args, _stream_of(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream_of(device))
+    if status != OK:
+        _check(status)
+
+
+def _device_of(name: str, t: torch.Tensor) -> int:
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return d
+
+
+def _reject(name: str, t: torch.Tensor, device: int, dtype: torch.dtype, shape) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} is {list(t.shape)}, not {list(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need(name: str, t: torch.Tensor, device: int, dtype: torch.dtype, shape) -> None:
+    """A dense tensor of this device, type and shape (None: any)."""
+    if (t.get_device() != device or t.dtype != dtype or not t.is_contiguous()
+            or (shape is not None and t.shape != shape)):
+        _reject(name, t, device, dtype, shape)
+
+
 def _token_stride(name: str, t: torch.Tensor) -> int:
     """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
     heads are dense (a slice of a packed projection is)."""
@@ -332,38 +381,36 @@ def _token_stride(name: str, t: torch.Tensor) -> int:
     n, h, d = t.shape
     if t.numel() == 0:
         return h * d
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name}'s heads must be dense (strides {t.stride()})")
-    if n > 1 and t.stride(0) < h * d:
+    if n > 1 and st < h * d:
         raise ValueError(f"{name}'s tokens overlap (strides {t.stride()})")
-    return t.stride(0) if n > 1 else h * d
+    return st if n > 1 else h * d
 
 
-def _check_device(named) -> None:
-    """Every (name, tensor) lies on the first one's CUDA device."""
-    dev = None
-    for name, t in named:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-
-
-def _check_int32(name: str, t: torch.Tensor, shape) -> None:
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be int32 {list(shape)}")
-
-
-def _paged_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, heads_dim: int) -> _PagedCache:
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, device: int, dtype: torch.dtype,
+          head_dim: int) -> _PagedCache:
+    code = DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; use torch.float32 or torch.bfloat16")
+    if k_pages.dim() != 4:
         raise ValueError("k_pages and v_pages must be [pages, n_kv_heads, page_size, head_dim]")
-    if k_pages.shape[3] != heads_dim:
-        raise ValueError(f"the pages hold heads of {k_pages.shape[3]}, q heads of {heads_dim}")
     n, hk, page, d = k_pages.shape
-    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, page, hk, d,
-                       _dtype_code(k_pages, v_pages))
+    if d != head_dim:
+        raise ValueError(f"the pages hold heads of {d}, q heads of {head_dim}")
+    _need("k_pages", k_pages, device, dtype, None)
+    _need("v_pages", v_pages, device, dtype, k_pages.shape)
+    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, page, hk, d, code)
+
+
+def _table(name: str, t: torch.Tensor, device: int, rows: int) -> int:
+    """Checks an int32 [rows, pages] table; returns its pages a row."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be int32 [{rows}, pages]")
+    width = t.shape[1]
+    _need(name, t, device, torch.int32, (rows, width))
+    return width
 
 
 def mrope_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
@@ -379,41 +426,38 @@ def mrope_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: t
     kv_lens[s] cache positions in the pages block_table[s]; its tokens are the
     last of them.  q, k and v may be slices of one packed projection (dense
     heads, any token stride).  Returns ``q_out``."""
-    if q_out is None:
-        q_out = q
-    _check_device((("q", q), ("k", k), ("v", v), ("pos", pos), ("q_start", q_start),
-                   ("kv_lens", kv_lens), ("block_table", block_table), ("k_pages", k_pages),
-                   ("v_pages", v_pages), ("q_out", q_out)))
-    weights = tuple((n, g) for n, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k))
-                    if g is not None)
-    _check_tensors((("pos", pos), ("q_start", q_start), ("kv_lens", kv_lens),
-                    ("block_table", block_table), ("k_pages", k_pages), ("v_pages", v_pages))
-                   + weights)
-    strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
+    device, dtype = _device_of("q", q), q.dtype
+    sq, sk, sv = _token_stride("q", q), _token_stride("k", k), _token_stride("v", v)
     tokens, hq, d = q.shape
-    cache = _paged_cache(k_pages, v_pages, d)
-    if k.shape != (tokens, cache.n_kv_heads, d) or v.shape != k.shape or q_out.shape != q.shape:
-        raise ValueError("shape mismatch")
-    if any(g.shape != (d,) for _, g in weights):
-        raise ValueError("gamma_q and gamma_k must be [head_dim]")
-    n_seqs = kv_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be int32 [n_seqs, max_pages]")
-    _check_int32("pos", pos, (3, tokens))
-    _check_int32("q_start", q_start, (n_seqs + 1,))
-    _check_int32("kv_lens", kv_lens, (n_seqs,))
-    _check_int32("block_table", block_table, (n_seqs, block_table.shape[1]))
-    _dtype_code(q, k, v, q_out, k_pages, *(g for _, g in weights))
-    batch = _PagedBatch(q_start.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n_seqs,
-                        block_table.shape[1])
-    sec = (_i32 * 3)(*[int(s) for s in sections])
-    with torch.cuda.device(q.device):
-        _check(lib().arops_mrope_paged_append(
-            q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
-            q_out.data_ptr(), strides[3], ctypes.byref(cache), ctypes.byref(batch),
-            None if gamma_q is None else gamma_q.data_ptr(),
-            None if gamma_k is None else gamma_k.data_ptr(), float(eps), pos.data_ptr(), tokens,
-            hq, sec, float(theta), _stream(q)))
+    if q_out is None:
+        q_out, so = q, sq
+    else:
+        so = _token_stride("q_out", q_out)
+        if q_out.get_device() != device or q_out.dtype != dtype or q_out.shape != q.shape:
+            _reject("q_out", q_out, device, dtype, q.shape)
+    cache = _pool(k_pages, v_pages, device, dtype, d)
+    shape = (tokens, cache.n_kv_heads, d)
+    if k.get_device() != device or k.dtype != dtype or k.shape != shape:
+        _reject("k", k, device, dtype, shape)
+    if v.get_device() != device or v.dtype != dtype or v.shape != shape:
+        _reject("v", v, device, dtype, shape)
+    gq = gk = None
+    if gamma_q is not None:
+        _need("gamma_q", gamma_q, device, dtype, (d,))
+        gq = gamma_q.data_ptr()
+    if gamma_k is not None:
+        _need("gamma_k", gamma_k, device, dtype, (d,))
+        gk = gamma_k.data_ptr()
+    n = kv_lens.numel()
+    i32 = torch.int32
+    _need("pos", pos, device, i32, (3, tokens))
+    _need("q_start", q_start, device, i32, (n + 1,))
+    _need("kv_lens", kv_lens, device, i32, (n,))
+    pages = _table("block_table", block_table, device, n)
+    batch = _PagedBatch(q_start.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, pages)
+    _launch(device, lib().arops_mrope_paged_append, q.data_ptr(), sq, k.data_ptr(), sk,
+            v.data_ptr(), sv, q_out.data_ptr(), so, cache, batch, gq, gk, eps, pos.data_ptr(),
+            tokens, hq, (_i32 * 3)(*sections), theta)
     return q_out
 
 
@@ -437,45 +481,33 @@ def attention_prepare(workspace: torch.Tensor) -> torch.Tensor:
 
 
 def _attention_args(q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes,
-                    bidir_lens, workspace, out, extra):
+                    bidir_lens, workspace, out):
     """Checks and arguments that both attention operators share."""
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, head_dim]")
-    tokens, hq, d = q.shape
-    if out is None:
-        out = torch.empty(tokens, hq, d, dtype=q.dtype, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(attention_workspace(tokens, hq, d), dtype=torch.uint8,
-                                device=q.device)
-        if q.is_cuda:
-            attention_prepare(workspace)
-    optional = tuple((n, t) for n, t in (("slopes", slopes), ("bidir_lens", bidir_lens))
-                     if t is not None)
-    dense = (("k_pages", k_pages), ("v_pages", v_pages), ("kv_lens", kv_lens),
-             ("block_table", block_table), ("workspace", workspace), ("out", out)
-             ) + optional + extra
-    _check_device((("q", q),) + dense)
-    _check_tensors(dense)
+    device, dtype = _device_of("q", q), q.dtype
     stride = _token_stride("q", q)
-    cache = _paged_cache(k_pages, v_pages, d)
-    _dtype_code(q, out, k_pages)
-    n_seqs = kv_lens.numel()
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be int32 [n_seqs, max_pages]")
-    _check_int32("kv_lens", kv_lens, (n_seqs,))
-    _check_int32("block_table", block_table, (n_seqs, block_table.shape[1]))
-    if slopes is not None and (slopes.dtype != torch.float32 or tuple(slopes.shape) != (hq,)):
-        raise ValueError("slopes must be float32 [n_q_heads]")
+    tokens, hq, d = q.shape
+    cache = _pool(k_pages, v_pages, device, dtype, d)
+    if out is None:
+        out = torch.empty(tokens, hq, d, dtype=dtype, device=q.device)
+    else:
+        _need("out", out, device, dtype, q.shape)
+    n = kv_lens.numel()
+    _need("kv_lens", kv_lens, device, torch.int32, (n,))
+    pages = _table("block_table", block_table, device, n)
+    options = _AttentionOptions(d ** -0.5 if scale is None else scale, softcap, window, None, None)
+    if slopes is not None:
+        _need("slopes", slopes, device, torch.float32, (hq,))
+        options.slopes = slopes.data_ptr()
     if bidir_lens is not None:
-        _check_int32("bidir_lens", bidir_lens, (n_seqs,))
-    options = _AttentionOptions(float(d ** -0.5 if scale is None else scale), float(softcap),
-                                int(window), None if slopes is None else slopes.data_ptr(),
-                                None if bidir_lens is None else bidir_lens.data_ptr())
-    batch = _PagedBatch(None, kv_lens.data_ptr(), block_table.data_ptr(), n_seqs,
-                        block_table.shape[1])
-    return stride, cache, batch, options, workspace, out
+        _need("bidir_lens", bidir_lens, device, torch.int32, (n,))
+        options.bidir_lens = bidir_lens.data_ptr()
+    if workspace is None:
+        workspace = attention_prepare(torch.empty(attention_workspace(tokens, hq, d),
+                                                  dtype=torch.uint8, device=q.device))
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        _reject("workspace", workspace, device, workspace.dtype, None)
+    batch = _PagedBatch(None, kv_lens.data_ptr(), block_table.data_ptr(), n, pages)
+    return device, stride, cache, batch, options, workspace, out
 
 
 def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -493,16 +525,13 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     slope * distance.  ``scale`` defaults to D ** -0.5.  ``workspace`` is a
     uint8 tensor of attention_workspace() bytes, cleared once
     (attention_prepare); allocated and cleared here if omitted."""
-    stride, cache, batch, options, workspace, out = _attention_args(
+    device, stride, cache, batch, options, workspace, out = _attention_args(
         q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes, bidir_lens,
-        workspace, out, (("q_start", q_start),))
-    _check_int32("q_start", q_start, (batch.n_seqs + 1,))
+        workspace, out)
+    _need("q_start", q_start, device, torch.int32, (batch.n_seqs + 1,))
     batch.q_start = q_start.data_ptr()
-    with torch.cuda.device(q.device):
-        _check(lib().arops_paged_attention(
-            q.data_ptr(), stride, out.data_ptr(), ctypes.byref(cache), ctypes.byref(batch),
-            ctypes.byref(options), q.shape[0], q.shape[1], workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(q)))
+    _launch(device, lib().arops_paged_attention, q.data_ptr(), stride, out.data_ptr(), cache,
+            batch, options, q.shape[0], q.shape[1], workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -519,25 +548,19 @@ def shared_prefix_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     group_start[g]..group_start[g+1], pages prefix_table[g]) and then its own
     kv_lens[s] positions (pages block_table[s]), at whose end it stands.
     Options, workspace and ``out`` as for paged_attention."""
-    stride, cache, batch, options, workspace, out = _attention_args(
+    device, stride, cache, batch, options, workspace, out = _attention_args(
         q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes, None,
-        workspace, out, (("group_start", group_start), ("prefix_lens", prefix_lens),
-                         ("prefix_table", prefix_table)))
+        workspace, out)
     if q.shape[0] != batch.n_seqs:
         raise ValueError("q must hold one token per sequence")
-    n_groups = prefix_lens.numel()
-    if prefix_table.dim() != 2:
-        raise ValueError("prefix_table must be int32 [n_groups, max_prefix_pages]")
-    _check_int32("group_start", group_start, (n_groups + 1,))
-    _check_int32("prefix_lens", prefix_lens, (n_groups,))
-    _check_int32("prefix_table", prefix_table, (n_groups, prefix_table.shape[1]))
-    groups = _PrefixGroups(group_start.data_ptr(), prefix_lens.data_ptr(),
-                           prefix_table.data_ptr(), n_groups, prefix_table.shape[1])
-    with torch.cuda.device(q.device):
-        _check(lib().arops_shared_prefix_attention(
-            q.data_ptr(), stride, out.data_ptr(), ctypes.byref(cache), ctypes.byref(batch),
-            ctypes.byref(groups), ctypes.byref(options), q.shape[1], workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(q)))
+    n = prefix_lens.numel()
+    _need("group_start", group_start, device, torch.int32, (n + 1,))
+    _need("prefix_lens", prefix_lens, device, torch.int32, (n,))
+    pages = _table("prefix_table", prefix_table, device, n)
+    groups = _PrefixGroups(group_start.data_ptr(), prefix_lens.data_ptr(), prefix_table.data_ptr(),
+                           n, pages)
+    _launch(device, lib().arops_shared_prefix_attention, q.data_ptr(), stride, out.data_ptr(),
+            cache, batch, groups, options, q.shape[1], workspace.data_ptr(), workspace.nbytes)
     return out
 
 

@@ -1342,18 +1342,24 @@ cudaError_t launch_tiles_f(const AttentionParams& p, const TilePlan& plan, const
                            const CUtensorMap& vmap, const CUtensorMap& qmap, int sm_count,
                            cudaStream_t st)
 {
-    auto kernel = attention_tiles_kernel<DP, FULL, SHARED>;
-    int ctas = 0;
+    constexpr auto kernel = attention_tiles_kernel<DP, FULL, SHARED>;
     constexpr int kSmem = tile_smem<DP>();
     static_assert(kSmem <= (int)kMaxSmemPerCta, "shared memory of a CTA");
-    cudaError_t err = resident_ctas(kernel, kTileThreads, kSmem, &ctas);
-    if (err != cudaSuccess)
-        return err;
-    if (ctas < 1)
-        return cudaErrorNotSupported;
     // one CTA an SM: each takes all of its SM's tensor memory
     const int grid = std::min(sm_count, kMaxTileCtas);
-    err = launch(kernel, dim3(grid), dim3(kTileThreads), kSmem, st, p, plan, kmap, vmap, qmap);
+    cudaError_t err = cudaSuccess;
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        int ctas = 0;
+        err = resident_ctas_once<kernel>(kTileThreads, kSmem, &ctas, attempt > 0);
+        if (err != cudaSuccess)
+            return err;
+        if (ctas < 1)
+            return cudaErrorNotSupported;
+        err = launch(kernel, dim3(grid), dim3(kTileThreads), kSmem, st, p, plan, kmap, vmap, qmap);
+        if (err != cudaErrorInvalidValue)
+            break;
+        cudaGetLastError();  // not kept for the caller's next call
+    }
     if (err != cudaSuccess)
         return err;
     return launch(attention_join_kernel<DP, SHARED>, dim3(grid, 2, DP / 32), dim3(kSubRows), 0, st,

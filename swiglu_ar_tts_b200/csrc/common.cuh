@@ -227,6 +227,31 @@ cudaError_t resident_ctas(K kernel, int threads, size_t smem, int* ctas)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, threads, smem);
 }
 
+// resident_ctas() once a kernel and device: its runtime calls cost a few
+// microseconds of every launch otherwise.  (The kernel's attributes belong to
+// the context; after a device reset a launch that needs them is refused, and
+// `forget` looks them up anew.)
+template <auto Kernel>
+cudaError_t resident_ctas_once(int threads, size_t smem, int* ctas, bool forget = false)
+{
+    constexpr int kMost = 64;
+    static std::atomic<int> known[kMost];  // 0: not looked up
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    const bool kept = dev >= 0 && dev < kMost;
+    if (kept && !forget) {
+        *ctas = known[dev].load(std::memory_order_acquire);
+        if (*ctas > 0)
+            return cudaSuccess;
+    }
+    err = resident_ctas(Kernel, threads, smem, ctas);
+    if (err == cudaSuccess && kept)
+        known[dev].store(*ctas, std::memory_order_release);
+    return err;
+}
+
 // CTAs of `Kernel` (at `threads` threads per CTA, no dynamic shared memory)
 // that `waves` full waves fill on a device of `sm_count` SMs.  The resident
 // CTAs per SM are looked up once per kernel (every device this library runs on

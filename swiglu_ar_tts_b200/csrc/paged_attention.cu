@@ -27,7 +27,6 @@
 // arrive joins the parts in their order along the keys, so arrival changes no
 // bit.  No CTA waits for another.
 #include "attention_common.cuh"
-#include <stdlib.h>
 
 namespace arops {
 namespace {
@@ -1107,13 +1106,21 @@ cudaError_t launch_rows(const AttentionParams& p, const RowPlan& plan, int sm_co
                         cudaStream_t st)
 {
     using R = RowTraits<T, DP>;
-    auto kernel = attention_rows_kernel<T, DP, VEC, FULL, SHARED>;
-    int ctas = 0;
-    cudaError_t err = resident_ctas(kernel, kRowThreads, R::kSmem, &ctas);
-    if (err != cudaSuccess)
-        return err;
-    const int64_t grid = std::min<int64_t>((int64_t)sm_count * std::max(ctas, 1), kMaxRowCtas);
-    return launch(kernel, dim3((unsigned)grid), dim3(kRowThreads), R::kSmem, st, p, plan);
+    constexpr auto kernel = attention_rows_kernel<T, DP, VEC, FULL, SHARED>;
+    cudaError_t err = cudaSuccess;
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        int ctas = 0;
+        err = resident_ctas_once<kernel>(kRowThreads, R::kSmem, &ctas, attempt > 0);
+        if (err != cudaSuccess)
+            return err;
+        const int64_t grid =
+            std::min<int64_t>((int64_t)sm_count * std::max(ctas, 1), kMaxRowCtas);
+        err = launch(kernel, dim3((unsigned)grid), dim3(kRowThreads), R::kSmem, st, p, plan);
+        if (err != cudaErrorInvalidValue)
+            return err;
+        cudaGetLastError();  // not kept for the caller's next call
+    }
+    return err;
 }
 
 template <typename T, int DP, bool VEC>
@@ -1187,7 +1194,7 @@ cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* 
     plan.g = make_row_divide(g);
     plan.seqs_a_tile = std::max(1, kRows / g);
     plan.tiles_a_seq = (int32_t)ceil_div(g, kRows);
-    plan.min_units = getenv("MINU") ? atoi(getenv("MINU")) : 1;
+    plan.min_units = 2;
 
     // Many rows a key go to the tile kernel: all of a ragged batch, or the
     // prefixes of a shared one (a window cuts prefixes row by row: the row

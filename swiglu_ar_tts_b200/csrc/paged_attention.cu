@@ -37,6 +37,10 @@ constexpr int kUnit = 64;   // keys of a unit
 constexpr int kBlock = 16;  // of which a warp takes
 constexpr int kRows = 16;   // rows of a tile
 
+// A pair's place on the line is kRowPairCost positions for its fixed cost (its
+// queries, the joins, its results: that of about as many units), then its units.
+constexpr int kRowPairCost = 2;
+
 __host__ __device__ constexpr int padded_head_dim(int d)
 {
     return d <= 64 ? 64 : d <= 128 ? 128 : 256;
@@ -138,11 +142,13 @@ struct RowTraits {
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kHalf = kBlock * kRowBytes;      // a warp's keys (or values)
     static constexpr int kStage = 2 * kHalf;
-    // Stages of a warp's ring and CTAs an SM: 128 KB (bf16, D <= 128: 2 x 4 x 3
-    // x 8 KB, two thirds of it in flight) to 192 KB an SM, above the ~64 KB
-    // that 44 GB/s an SM need at ~1 us of latency.
-    static constexpr int kStages = 3;
-    static constexpr int kCtas = kStage <= 4096 ? 4 : kStage <= 8192 ? 2 : 1;
+    // Stages of a warp's ring and CTAs an SM: 96 KB in flight an SM, above the
+    // ~64 KB that 44 GB/s an SM need at ~1 us of latency.  bf16 heads of 128:
+    // three CTAs of two stages, the third to fill the other two's changes of
+    // sequence; two of three stages measured 354 against 344 us (256 sequences
+    // of 60-4,100 keys), three stages being more than the loads need.
+    static constexpr int kStages = kStage == 8192 ? 2 : 3;
+    static constexpr int kCtas = kStage <= 4096 ? 4 : kStage <= 8192 ? 3 : 1;
     static constexpr int kSteps = kE == 2 ? DP / 16 : DP / 8;  // of the first product
     static constexpr int kQWords = kE == 2 ? 4 : 8;            // a lane's fragment words a step
     static constexpr int kQBytes = kSteps * 32 * kQWords * 4;
@@ -155,7 +161,7 @@ struct Cursor {
     int32_t seq;   // first sequence of the tile
     int32_t sub;   // tile within the sequence
     int32_t kvh;   // key head
-    int32_t unit;  // unit within the (tile, key head) pair
+    int32_t unit;  // units of the pair before the share (negative: in its fixed cost)
 };
 
 // Keys of one (tile, key head) pair.  Lane m < 16 holds member m's length in
@@ -228,8 +234,9 @@ __device__ __forceinline__ int32_t own_first(const AttentionParams& p, int32_t p
     return max(lo - prefix, 0) & ~(kUnit - 1);
 }
 
-// Units that sequence s adds to the line (per key head): its own, once a tile
-// of its heads, and the prefix's if it is its tile's first member.
+// What sequence s adds to the line (per key head): its own units, once a tile of
+// its heads, and, if it is its tile's first member, the prefix's and the fixed
+// cost.
 __device__ __forceinline__ int64_t member_units(const AttentionParams& p, const RowPlan& plan,
                                                 int32_t s, const Member& m, bool& bad)
 {
@@ -254,12 +261,12 @@ __device__ __forceinline__ int64_t member_units(const AttentionParams& p, const 
             }
             rest = any ? 0 : 1;
         }
-        n += rest;
+        n += rest + kRowPairCost;
     }
     return n * plan.tiles_a_seq;
 }
 
-// Units (of one key head) that sequence s adds to the line.
+// What sequence s adds to the line, for one key head.
 template <bool SHARED>
 __device__ __forceinline__ int64_t sequence_units(const AttentionParams& p, const RowPlan& plan,
                                                   int32_t s, bool& bad)
@@ -274,7 +281,7 @@ __device__ __forceinline__ int64_t sequence_units(const AttentionParams& p, cons
         for (int32_t i = 0; i < tiles; ++i) {
             int32_t lo, hi;
             ragged_range<kUnit>(p, r, plan.g, i * kRows, kRows, lo, hi);
-            n += max(1, units_between<kUnit>(lo, hi));
+            n += max(1, units_between<kUnit>(lo, hi)) + kRowPairCost;
         }
         return n;
     }
@@ -543,30 +550,38 @@ __device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const 
     };
     const int row = threadIdx.x % kRows, lead = threadIdx.x / kRows;
     constexpr int kLeads = kRowThreads / kRows;
-    // every row's m and l: kLeads threads a row, then theirs joined
-    float m = -INFINITY, l = 0.0f;
-    if (row_at[row].token >= 0) {
-        for (int32_t x = cta0 + lead; x <= cta1; x += 4 * kLeads) {
-            float mx[4], lx[4];
+    float4 v[4][kItems];
+    auto load4 = [&](int32_t x) {  // four parts' share of this thread, from x
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool in = x + i * kLeads <= cta1;
-                const float* src = part_of(in ? x + i * kLeads : x) + kRows * DP + row;
-                mx[i] = in ? __ldcg(src) : -INFINITY;
-                lx[i] = in ? __ldcg(src + kRows) : 0.0f;
-            }
+        for (int j = 0; j < 4; ++j) {
+            const float* src = part_of(min(x + j, cta1));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float mn = fmaxf(m, mx[i]);
-                if (mx[i] != -INFINITY)
-                    l = (m == -INFINITY ? 0.0f : l * exp2_fast(m - mn)) +
-                        lx[i] * exp2_fast(mx[i] - mn);
-                m = mn;
+            for (int i = 0; i < kItems; ++i) {
+                const int idx = threadIdx.x + i * kRowThreads;
+                v[j][i] = x + j <= cta1 && row_at[idx / (DP / 4)].token >= 0
+                              ? __ldcg(reinterpret_cast<const float4*>(src) + idx)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
         }
+    };
+    load4(cta0);
+    // every row's m and l: kLeads threads a row, then theirs joined
+    const bool few = cta1 - cta0 < kMost;
+    float m = -INFINITY, l = 0.0f;
+    for (int32_t x = cta0 + lead; x <= cta1; x += kLeads) {
+        const bool in = row_at[row].token >= 0;
+        const float* src = part_of(x) + kRows * DP + row;
+        const float mx = in ? __ldcg(src) : -INFINITY;
+        const float lx = in ? __ldcg(src + kRows) : 0.0f;
+        if (few)
+            weights[(x - cta0) * kRows + row] = mx;
+        const float mn = fmaxf(m, mx);
+        if (mx != -INFINITY)
+            l = (m == -INFINITY ? 0.0f : l * exp2_fast(m - mn)) + lx * exp2_fast(mx - mn);
+        m = mn;
     }
-    float* lead_m = weights;
-    float* lead_l = weights + kRowThreads;
+    float* lead_m = weights + kMost * kRows;
+    float* lead_l = lead_m + kRowThreads;
     lead_m[threadIdx.x] = m;
     lead_l[threadIdx.x] = l;
     __syncthreads();
@@ -592,25 +607,17 @@ __device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const 
         __syncthreads();
         for (int i = threadIdx.x; i < n * kRows; i += kRowThreads) {
             const int r = i % kRows;
-            const float mx = row_at[r].token >= 0
-                                 ? __ldcg(part_of(x0 + i / kRows) + kRows * DP + r)
-                                 : -INFINITY;
+            float mx = -INFINITY;
+            if (few)
+                mx = weights[i];
+            else if (row_at[r].token >= 0)
+                mx = __ldcg(part_of(x0 + i / kRows) + kRows * DP + r);
             weights[i] = mx == -INFINITY ? 0.0f : exp2_fast(mx - row_m[0][r]);
         }
         __syncthreads();
         for (int y = 0; y < n; y += 4) {
-            float4 v[4][kItems];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float* src = part_of(x0 + min(y + j, n - 1));
-#pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    const int idx = threadIdx.x + i * kRowThreads;
-                    v[j][i] = y + j < n && row_at[idx / (DP / 4)].token >= 0
-                                  ? __ldcg(reinterpret_cast<const float4*>(src) + idx)
-                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                }
-            }
+            if (x0 + y > cta0)
+                load4(x0 + y);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -660,9 +667,16 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
     const int32_t per = (p.n_seqs + kRowThreads - 1) / kRowThreads;
     const int32_t s_begin = min((int64_t)threadIdx.x * per, (int64_t)p.n_seqs);
     const int32_t s_end = min(s_begin + per, p.n_seqs);
+    // (kept in shared memory as far as it reaches, for the search below)
+    int64_t* counted = reinterpret_cast<int64_t*>(smem);
+    const bool keeps = p.n_seqs <= (int)(R::kRing / sizeof(int64_t));
     int64_t mine = 0;
-    for (int32_t s = s_begin; s < s_end; ++s)
-        mine += sequence_units<SHARED>(p, plan, s, bad);
+    for (int32_t s = s_begin; s < s_end; ++s) {
+        const int64_t n = sequence_units<SHARED>(p, plan, s, bad);
+        if (keeps)
+            counted[s] = n;
+        mine += n;
+    }
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -701,15 +715,18 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
     const int64_t begin = (int64_t)blockIdx.x * share;
     if (begin >= line)
         return;
-    int64_t left = min(share, line - begin);
+    const int64_t end = min(begin + share, line);
     {
         int64_t before = upto - mine;
         if (begin >= before * p.hk && begin < upto * p.hk) {
-            int32_t s = s_begin;
             bool ignore = false;
+            auto count = [&](int32_t x) {
+                return keeps ? counted[x] : sequence_units<SHARED>(p, plan, x, ignore);
+            };
+            int32_t s = s_begin;
             int64_t n = 0;
             for (;; ++s) {
-                n = sequence_units<SHARED>(p, plan, s, ignore);
+                n = count(s);
                 if (begin < (before + n) * p.hk)
                     break;
                 before += n;
@@ -717,56 +734,69 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
             Cursor c;
             c.seq = s;
             c.sub = 0;
-            int64_t tile_units = 1;
+            int64_t tile_line = n;
             if constexpr (SHARED) {
                 // back to the tile's first member, then into the tile of its heads
                 const Member m = find_member(p, s, ignore);
-                c.seq = s - m.index % plan.seqs_a_tile;
-                int64_t all = n;
-                for (int32_t x = c.seq; x < s; ++x) {
-                    const Member mx = find_member(p, x, ignore);
-                    const int64_t u = member_units(p, plan, x, mx, ignore);
-                    before -= u;
-                    all += u;
+                const int32_t in_tile = m.index % plan.seqs_a_tile;
+                c.seq = s - in_tile;
+                const int32_t end = c.seq + min(plan.seqs_a_tile, m.count - m.index + in_tile);
+                tile_line = 0;
+                for (int32_t x = c.seq; x < end; ++x) {
+                    const int64_t u = x == s ? n : count(x);
+                    if (x < s)
+                        before -= u;
+                    tile_line += u;
                 }
-                const int32_t members = min(plan.seqs_a_tile, m.count - (c.seq - (s - m.index)));
-                for (int32_t x = s + 1; x < c.seq + members; ++x) {
-                    const Member mx = find_member(p, x, ignore);
-                    all += member_units(p, plan, x, mx, ignore);
-                }
-                tile_units = all / plan.tiles_a_seq;
-                c.sub = (int32_t)((begin / p.hk - before) / tile_units);
-                before += c.sub * tile_units;
+                tile_line /= plan.tiles_a_seq;
+                c.sub = (int32_t)((begin / p.hk - before) / tile_line);
+                before += c.sub * tile_line;
             } else {
                 const Ragged r = load_ragged(p, s, ignore);
-                for (;; ++c.sub) {
-                    int32_t lo, hi;
-                    ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, lo, hi);
-                    tile_units = max(1, units_between<kUnit>(lo, hi));
-                    if (begin < (before + tile_units) * p.hk)
-                        break;
-                    before += tile_units;
-                }
+                if (ragged_tiles(r, plan.g) > 1)
+                    for (;; ++c.sub) {
+                        int32_t lo, hi;
+                        ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, lo, hi);
+                        tile_line = max(1, units_between<kUnit>(lo, hi)) + kRowPairCost;
+                        if (begin < (before + tile_line) * p.hk)
+                            break;
+                        before += tile_line;
+                    }
             }
             const int64_t rest = begin - before * p.hk;
-            c.kvh = (int32_t)(rest / tile_units);
-            c.unit = (int32_t)(rest % tile_units);
+            c.kvh = (int32_t)(rest / tile_line);
+            c.unit = (int32_t)(rest % tile_line) - kRowPairCost;
             found = c;
         }
     }
     __syncthreads();
     Cursor c = found;
-    int64_t at = begin;  // place of the cursor on the line
+    int64_t at = begin - c.unit;  // place of the pair's unit 0 on the line
 
-    while (left > 0 && c.seq < p.n_seqs) {
+    while (at < end && c.seq < p.n_seqs) {
         TileKeys k;
         if (!load_tile<SHARED>(p, plan, c, k, lane)) {
             ++c.seq;
             c.sub = 0;
             continue;
         }
-        const int32_t u0 = c.unit;
-        const int32_t u1 = (int32_t)min((int64_t)k.units, (int64_t)u0 + left);
+        const int32_t u0 = (int32_t)max(begin - at, (int64_t)0);
+        const int32_t u1 = (int32_t)min(end - at, (int64_t)k.units);
+        auto next_pair = [&]() {
+            at += k.units + kRowPairCost;
+            if (++c.kvh == p.hk) {
+                c.kvh = 0;
+                ++c.sub;
+                if (SHARED && c.sub >= plan.tiles_a_seq) {
+                    c.sub = 0;
+                    c.seq += k.ntok;
+                }
+            }
+        };
+        if (u0 >= u1) {
+            next_pair();
+            continue;
+        }
 
         // -- the tile's queries, and this lane's two rows ----------------------
         __syncthreads();  // the last pair's use of shared memory is over
@@ -1026,9 +1056,8 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
 
         const bool whole = u0 == 0 && u1 == k.units;
         // the pair's first unit on the line, its first and last CTA
-        const int64_t pair0 = at - u0;
-        const int32_t cta0 = (int32_t)(pair0 / share);
-        const int32_t cta1 = (int32_t)((pair0 + k.units - 1) / share);
+        const int32_t cta0 = (int32_t)(at / share);
+        const int32_t cta1 = (int32_t)((at + k.units - 1) / share);
         float* part = plan.parts +
                       ((int64_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * part_floats(DP);
         for (int idx = threadIdx.x; idx < kRows * DP / 4; idx += kRowThreads) {
@@ -1067,18 +1096,20 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
 
         // -- join the CTAs: the last to arrive does ---------------------------
         if (!whole) {
-            __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
                 const int32_t n = cta1 - cta0 + 1;
-                const int32_t old = atomicAdd(plan.counters + cta0, 1);
+                // releases what the barrier brought together, acquires the others'
+                int32_t old;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                             : "=r"(old)
+                             : "l"(plan.counters + cta0)
+                             : "memory");
                 if (old < 0 || old >= n)
                     record_device_error(p.err, AROPS_DEVICE_ERR_WORKSPACE);
                 last_flag = old == n - 1;
-                if (last_flag) {
+                if (last_flag)
                     plan.counters[cta0] = 0;
-                    __threadfence();
-                }
             }
             __syncthreads();
             if (last_flag)
@@ -1086,18 +1117,7 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                                           reinterpret_cast<float*>(smem));
         }
 
-        // -- on along the line -------------------------------------------------
-        left -= u1 - u0;
-        at += u1 - u0;
-        c.unit = 0;
-        if (++c.kvh == p.hk) {
-            c.kvh = 0;
-            ++c.sub;
-            if (SHARED && c.sub >= plan.tiles_a_seq) {
-                c.sub = 0;
-                c.seq += k.ntok;
-            }
-        }
+        next_pair();
     }
 }
 

@@ -41,6 +41,11 @@ constexpr int kRows = 16;   // rows of a tile
 // queries, the joins, its results: that of about as many units), then its units.
 constexpr int kRowPairCost = 2;
 
+// Least share of a CTA: with fewer units a share, a pair has more parts to join
+// than the units take (5 candidates on 1,100 positions: 24.5, 20.1, 18.3, 21.1,
+// 21.7 us with 1, 2, 3, 4, 6).
+constexpr int kMinUnits = 3;
+
 __host__ __device__ constexpr int padded_head_dim(int d)
 {
     return d <= 64 ? 64 : d <= 128 ? 128 : 256;
@@ -536,35 +541,21 @@ __device__ __forceinline__ void store_result(const AttentionParams& p, const Row
 }
 
 // Joins the parts of CTAs cta0 .. cta1 in their order: 2^(m_x - m) O_x summed
-// over x, likewise l.  Latency is all that counts here (a part comes out of
-// L2), so a thread takes its share of the tile's columns of four parts at once.
+// over x, likewise l.  Latency is all that counts here (parts come out of L2,
+// instructions too: this runs once a CTA at most), so it is short code with
+// eight parts on their way.
 template <typename T, int DP, bool SHARED>
 __device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const RowOf* row_at,
                            int32_t cta0, int32_t cta1, float (*row_m)[kRows],
                            float (*row_l)[kRows], float* weights)
 {
-    constexpr int kItems = kRows * DP / 4 / kRowThreads;
-    constexpr int kMost = 64;  // parts whose weights are in shared memory at a time
+    constexpr int kMost = 64;  // parts whose weights fit in shared memory
+    constexpr int kBatch = 8;  // parts a thread asks for at once
     auto part_of = [&](int32_t x) {
         return plan.parts + ((int64_t)x * 2 + (x == cta0 ? 1 : 0)) * part_floats(DP);
     };
     const int row = threadIdx.x % kRows, lead = threadIdx.x / kRows;
     constexpr int kLeads = kRowThreads / kRows;
-    float4 v[4][kItems];
-    auto load4 = [&](int32_t x) {  // four parts' share of this thread, from x
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float* src = part_of(min(x + j, cta1));
-#pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int idx = threadIdx.x + i * kRowThreads;
-                v[j][i] = x + j <= cta1 && row_at[idx / (DP / 4)].token >= 0
-                              ? __ldcg(reinterpret_cast<const float4*>(src) + idx)
-                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-        }
-    };
-    load4(cta0);
     // every row's m and l: kLeads threads a row, then theirs joined
     const bool few = cta1 - cta0 < kMost;
     float m = -INFINITY, l = 0.0f;
@@ -598,47 +589,45 @@ __device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const 
         row_m[0][row] = m;
         row_l[0][row] = l;
     }
-    float sum[kItems][4];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-        sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.0f;
-    for (int32_t x0 = cta0; x0 <= cta1; x0 += kMost) {
-        const int n = min(kMost, cta1 - x0 + 1);
-        __syncthreads();
-        for (int i = threadIdx.x; i < n * kRows; i += kRowThreads) {
-            const int r = i % kRows;
-            float mx = -INFINITY;
-            if (few)
-                mx = weights[i];
-            else if (row_at[r].token >= 0)
-                mx = __ldcg(part_of(x0 + i / kRows) + kRows * DP + r);
-            weights[i] = mx == -INFINITY ? 0.0f : exp2_fast(mx - row_m[0][r]);
+    __syncthreads();
+    if (few)
+        for (int i = threadIdx.x; i < (cta1 - cta0 + 1) * kRows; i += kRowThreads) {
+            const float mx = weights[i];
+            weights[i] = mx == -INFINITY ? 0.0f : exp2_fast(mx - row_m[0][i % kRows]);
         }
-        __syncthreads();
-        for (int y = 0; y < n; y += 4) {
-            if (x0 + y > cta0)
-                load4(x0 + y);
+    __syncthreads();
+#pragma unroll 1
+    for (int idx = threadIdx.x; idx < kRows * DP / 4; idx += kRowThreads) {
+        const int at = idx / (DP / 4), e = idx % (DP / 4) * 4;
+        const RowOf r = row_at[at];
+        if (r.token < 0 || e >= p.head_dim)
+            continue;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int32_t x = cta0; x <= cta1; x += kBatch) {
+            float4 v[kBatch];
+            float f[kBatch];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < kBatch; ++j) {
+                const int32_t y = min(x + j, cta1);
+                const float* src = part_of(y);
+                v[j] = __ldcg(reinterpret_cast<const float4*>(src) + idx);
+                f[j] = few ? weights[(y - cta0) * kRows + at]
+                           : __ldcg(src + kRows * DP + at);
+            }
 #pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    const int r = (threadIdx.x + i * kRowThreads) / (DP / 4);
-                    const float f = y + j < n ? weights[(y + j) * kRows + r] : 0.0f;
-                    sum[i][0] = fmaf(v[j][i].x, f, sum[i][0]);
-                    sum[i][1] = fmaf(v[j][i].y, f, sum[i][1]);
-                    sum[i][2] = fmaf(v[j][i].z, f, sum[i][2]);
-                    sum[i][3] = fmaf(v[j][i].w, f, sum[i][3]);
-                }
+            for (int j = 0; j < kBatch; ++j) {
+                if (!few)
+                    f[j] = f[j] == -INFINITY ? 0.0f : exp2_fast(f[j] - row_m[0][at]);
+                if (x + j > cta1)
+                    f[j] = 0.0f;
+                sum[0] = fmaf(v[j].x, f[j], sum[0]);
+                sum[1] = fmaf(v[j].y, f[j], sum[1]);
+                sum[2] = fmaf(v[j].z, f[j], sum[2]);
+                sum[3] = fmaf(v[j].w, f[j], sum[3]);
+            }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int idx = threadIdx.x + i * kRowThreads;
-        const RowOf r = row_at[idx / (DP / 4)];
-        const int e = idx % (DP / 4) * 4;
-        if (r.token >= 0 && e < p.head_dim)
-            store_result<T, DP, SHARED>(p, plan, r, e, sum[i], row_m[0][idx / (DP / 4)],
-                                        row_l[0][idx / (DP / 4)]);
+        store_result<T, DP, SHARED>(p, plan, r, e, sum, row_m[0][at], row_l[0][at]);
     }
 }
 
@@ -1214,7 +1203,7 @@ cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* 
     plan.g = make_row_divide(g);
     plan.seqs_a_tile = std::max(1, kRows / g);
     plan.tiles_a_seq = (int32_t)ceil_div(g, kRows);
-    plan.min_units = 2;
+    plan.min_units = kMinUnits;
 
     // Many rows a key go to the tile kernel: all of a ragged batch, or the
     // prefixes of a shared one (a window cuts prefixes row by row: the row

@@ -204,7 +204,9 @@ typedef struct {
  * All arrays are int32 on the device and are read when the kernel runs, so a
  * captured call follows their contents.  Tokens at and behind q_start[n_seqs]
  * belong to no sequence (a padded batch): nothing of theirs is written.
- * Block-table entries behind a sequence's last page are never looked at.
+ * Block-table entries behind a sequence's last page are never looked at, nor by
+ * attention those of pages that a window hides from all its queries.
+ * max_pages * page_size <= 2^31 - 1025.
  * Whatever the arrays hold, nothing out of range is read or written, and a
  * malformed entry sets AROPS_DEVICE_ERR_BAD_INDEX in the device error word: a
  * length above max_pages * page_size counts as that; a page outside the pool is
@@ -261,7 +263,7 @@ AROPS_API arops_status arops_mrope_paged_append(
  */
 typedef struct {
     float scale;               /* finite; 1/sqrt(head_dim) usually */
-    float softcap;             /* finite, >= 0; 0: no cap */
+    float softcap;             /* finite, >= 1e-30, or 0: no cap */
     int32_t window;            /* >= 0 positions, the query's own included; 0: no limit */
     const float* slopes;       /* [n_q_heads] float32 device array, or NULL */
     const int32_t* bidir_lens; /* [n_seqs] int32 device array, or NULL */

@@ -278,6 +278,10 @@ AROPS_API arops_status arops_mrope_kv_append(const void* q, const void* k, const
 
 namespace {
 
+// Positions of a sequence: the kernels step past the last one by less than this
+// leaves of 32 bits.
+constexpr int64_t kMaxPositions = INT32_MAX - 1024;
+
 // A pool of pages: its sizes, and (when it holds anything) its pointers.
 arops_status check_cache(const char* name, const arops_paged_cache* c, int32_t max_head_dim)
 {
@@ -310,9 +314,9 @@ arops_status check_batch(const char* name, const arops_paged_batch* b, const aro
         return fail(AROPS_ERR_INVALID, "%s: batch is null", name);
     if (tokens < 0 || b->n_seqs < 0 || b->max_pages < 0)
         return fail(AROPS_ERR_INVALID, "%s: negative size", name);
-    if (tokens > INT32_MAX || (int64_t)b->max_pages * c->page_size > INT32_MAX)
-        return fail(AROPS_ERR_UNSUPPORTED, "%s: tokens and max_pages * page_size must be < 2^31",
-                    name);
+    if (tokens > INT32_MAX || (int64_t)b->max_pages * c->page_size > kMaxPositions)
+        return fail(AROPS_ERR_UNSUPPORTED,
+                    "%s: supported tokens < 2^31, max_pages * page_size <= 2^31 - 1025", name);
     if (tokens == 0 || b->n_seqs == 0)
         return AROPS_OK;
     if ((needs_q_start && !b->q_start) || !b->kv_lens || (b->max_pages > 0 && !b->block_table))
@@ -371,10 +375,11 @@ arops_status attention_entry(const char* name, const void* q, int64_t q_stride, 
                     "%s: tokens * n_q_heads / n_kv_heads must be < 2^31", name);
     if (!opt)
         return fail(AROPS_ERR_INVALID, "%s: options is null", name);
-    if (!isfinite(opt->scale) || !isfinite(opt->softcap) || opt->softcap < 0.0f ||
-        opt->window < 0)
+    if (!isfinite(opt->scale) || !isfinite(opt->softcap) || opt->window < 0 ||
+        (opt->softcap != 0.0f && !(opt->softcap >= 1e-30f)))
         return fail(AROPS_ERR_INVALID,
-                    "%s: scale and softcap must be finite, softcap and window >= 0", name);
+                    "%s: scale and softcap must be finite, softcap 0 or >= 1e-30, window >= 0",
+                    name);
     st = check_stride(name, "q", q_stride, n_q_heads, cache->head_dim);
     if (st != AROPS_OK)
         return st;
@@ -383,9 +388,11 @@ arops_status attention_entry(const char* name, const void* q, int64_t q_stride, 
             return fail(AROPS_ERR_INVALID, "%s: negative size", name);
         if (opt->bidir_lens)
             return fail(AROPS_ERR_INVALID, "%s: bidir_lens must be null", name);
-        if (((int64_t)groups->max_prefix_pages + batch->max_pages) * cache->page_size > INT32_MAX)
+        if (((int64_t)groups->max_prefix_pages + batch->max_pages) * cache->page_size >
+            kMaxPositions)
             return fail(AROPS_ERR_UNSUPPORTED,
-                        "%s: (max_prefix_pages + max_pages) * page_size must be < 2^31", name);
+                        "%s: supported (max_prefix_pages + max_pages) * page_size <= 2^31 - 1025",
+                        name);
         if (groups->n_groups > batch->n_seqs)
             return fail(AROPS_ERR_INVALID, "%s: more groups (%d) than sequences (%d)", name,
                         (int)groups->n_groups, (int)batch->n_seqs);

@@ -120,19 +120,20 @@ __device__ __forceinline__ Ragged load_ragged(const AttentionParams& p, int32_t 
 }
 
 // Keys that some of rows [row0, row0 + n) sees; rows run over the tokens, g a
-// token.  The first row's keys begin first and the last row's end last.  lo is
-// rounded down to a unit.
+// token.  The first row's keys begin first (at `seen`) and the last row's end
+// last.  lo is `seen` rounded down to a unit.
 template <int UNIT>
 __device__ __forceinline__ void ragged_range(const AttentionParams& p, const Ragged& r,
                                              const RowDivide& g, uint32_t row0,
-                                             uint32_t n, int32_t& lo, int32_t& hi)
+                                             uint32_t n, int32_t& lo, int32_t& hi,
+                                             int32_t& seen)
 {
     const int32_t first = (int32_t)g(row0);
     const int32_t last = min(r.ntok - 1, (int32_t)g(row0 + n - 1));
     int32_t x;
-    visible_keys(r.len - r.ntok + first, r.len, r.bidir, p.window, lo, x);
+    visible_keys(r.len - r.ntok + first, r.len, r.bidir, p.window, seen, x);
     visible_keys(r.len - r.ntok + last, r.len, r.bidir, p.window, x, hi);
-    lo &= ~(UNIT - 1);
+    lo = seen & ~(UNIT - 1);
 }
 
 // The tile kernel (attention_tiles.cu).  With prefix_o it takes the prefixes of

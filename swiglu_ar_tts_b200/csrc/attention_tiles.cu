@@ -85,7 +85,7 @@ struct TileCursor {
 // Keys of one (tile, key head) pair and of its sub-tiles: units [jlo, jhi).
 struct TileSpan {
     int32_t tok0, ntok, len, bidir;
-    int32_t lo, units;
+    int32_t lo, first, units;  // first seen key, rounded down to a unit and not
     int32_t jlo[2], jhi[2];
     const int32_t* table;
 };
@@ -126,8 +126,8 @@ __device__ __forceinline__ int32_t tile_units(const AttentionParams& p, const Ra
     if constexpr (SHARED) {
         return max(1, units_between<kTileUnit>(0, r.len));
     } else {
-        int32_t lo, hi;
-        ragged_range<kTileUnit>(p, r, g, (uint32_t)sub * kTileRows, kTileRows, lo, hi);
+        int32_t lo, hi, first;
+        ragged_range<kTileUnit>(p, r, g, (uint32_t)sub * kTileRows, kTileRows, lo, hi, first);
         return max(1, units_between<kTileUnit>(lo, hi));
     }
 }
@@ -149,7 +149,7 @@ __device__ __forceinline__ bool load_span(const AttentionParams& p, const TilePl
     t.table = SHARED ? p.prefix_table + (int64_t)c.seq * p.max_prefix_pages
                      : p.block_table + (int64_t)c.seq * p.max_pages;
     const uint32_t rows = (uint32_t)r.ntok * g.n;
-    int32_t lo[2], hi[2];
+    int32_t lo[2], hi[2], first[2] = {0, 0};
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         const uint32_t row0 = (uint32_t)c.sub * kTileRows + w * kSubRows;
@@ -158,13 +158,14 @@ __device__ __forceinline__ bool load_span(const AttentionParams& p, const TilePl
             if constexpr (SHARED)
                 hi[w] = r.len;
             else
-                ragged_range<kTileUnit>(p, r, g, row0, kSubRows, lo[w], hi[w]);
+                ragged_range<kTileUnit>(p, r, g, row0, kSubRows, lo[w], hi[w], first[w]);
         } else if (w == 1) {
             lo[1] = lo[0];
             hi[1] = lo[0];
         }
     }
     t.lo = lo[0];
+    t.first = first[0];
     t.units = max(1, units_between<kTileUnit>(lo[0], max(hi[0], hi[1])));
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -224,7 +225,7 @@ struct TileWalk {
 
 // One pair's units of a CTA's share, as the roles see it.
 struct TilePiece {
-    int32_t tok0, ntok, len, bidir, lo;
+    int32_t tok0, ntok, len, bidir, lo, first;
     int32_t sub, kvh;
     int32_t u0, u1;          // units of the share; u0 == u1: the end
     int32_t a[2], b[2];      // of each sub-tile: [a, b)
@@ -337,9 +338,10 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
         for (int32_t u = t.u0; ok && u < t.u1; ++u) {
             const int32_t key0 = t.lo + u * kTileUnit;
             const int32_t key = key0 + lane * plan.box;
-            // a copy of a page that does not exist brings zeros
+            // a copy of a page that does not exist, or that nobody sees any of,
+            // brings zeros
             int32_t page = (int32_t)p.map.num_pages, slot = 0;
-            if (lane < boxes && key < t.len) {
+            if (lane < boxes && key < t.len && key + plan.box > t.first) {
                 int32_t pi;
                 split_position(p.map, key, pi, slot);
                 page = __ldg(t.table + pi);
@@ -490,6 +492,7 @@ __device__ void tile_query_role(const AttentionParams& p, const TilePlan& plan,
             t.len = s.len;
             t.bidir = s.bidir;
             t.lo = s.lo;
+            t.first = s.first;
             t.table = s.table;
             t.sub = walk.pair.sub;
             t.kvh = walk.pair.kvh;
@@ -666,7 +669,7 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const Score
             big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[i]))),
                         fabsf(__uint_as_float(s[i + 1])));
         const float in = map.scale * map.inv_cap, in2 = in * in;
-        if (__all_sync(0xFFFFFFFFu, big * fabsf(in) <= 0.5f)) {
+        if (__all_sync(0xFFFFFFFFu, big * fabsf(in) <= 0.5f && fabsf(in) < 1e5f)) {
             const float2 c0 = both(kTanh0 * out), c1 = both(kTanh1 * out * in2),
                          c2 = both(kTanh2 * out * (in2 * in2)),
                          c3 = both(kTanh3 * out * (in2 * in2 * in2));

@@ -173,7 +173,8 @@ struct Cursor {
 // shared-prefix tiles (units: prefix first, then each member's own).
 struct TileKeys {
     int32_t tok0;    // first token of the entity (a sequence, or a tile's members)
-    int32_t lo, hi;  // keys of the table at `table`: [lo, hi), lo a multiple of kUnit
+    int32_t lo, hi;  // keys [lo, hi) of the sequence (the prefix), lo a multiple of kUnit
+    int32_t seen;    // the first of them that a row sees
     int32_t len;     // sequence length, or prefix length
     int32_t ntok;    // query tokens, or members
     int32_t bidir;
@@ -223,20 +224,32 @@ __device__ __forceinline__ int32_t own_length(const AttentionParams& p, int32_t 
     return clamp_length(__ldg(p.kv_lens + s), p.max_pages * p.map.page_size, bad);
 }
 
-// First key of the prefix, and of the member's own keys, that the window leaves.
-__device__ __forceinline__ int32_t prefix_first(const AttentionParams& p, int32_t prefix,
-                                                int32_t own)
+// First key of the prefix, and of the member's own keys, that the window leaves
+// (..._first: of its unit).
+__device__ __forceinline__ int32_t prefix_seen(const AttentionParams& p, int32_t prefix,
+                                               int32_t own)
 {
     int32_t lo, hi;
     visible_keys(prefix + own - 1, prefix + own, 0, p.window, lo, hi);
-    return min(lo, prefix) & ~(kUnit - 1);
+    return min(lo, prefix);
+}
+
+__device__ __forceinline__ int32_t prefix_first(const AttentionParams& p, int32_t prefix,
+                                                int32_t own)
+{
+    return prefix_seen(p, prefix, own) & ~(kUnit - 1);
+}
+
+__device__ __forceinline__ int32_t own_seen(const AttentionParams& p, int32_t prefix, int32_t own)
+{
+    int32_t lo, hi;
+    visible_keys(prefix + own - 1, prefix + own, 0, p.window, lo, hi);
+    return max(lo - prefix, 0);
 }
 
 __device__ __forceinline__ int32_t own_first(const AttentionParams& p, int32_t prefix, int32_t own)
 {
-    int32_t lo, hi;
-    visible_keys(prefix + own - 1, prefix + own, 0, p.window, lo, hi);
-    return max(lo - prefix, 0) & ~(kUnit - 1);
+    return own_seen(p, prefix, own) & ~(kUnit - 1);
 }
 
 // What sequence s adds to the line (per key head): its own units, once a tile of
@@ -284,8 +297,8 @@ __device__ __forceinline__ int64_t sequence_units(const AttentionParams& p, cons
         const int32_t tiles = ragged_tiles(r, plan.g);
         int64_t n = 0;
         for (int32_t i = 0; i < tiles; ++i) {
-            int32_t lo, hi;
-            ragged_range<kUnit>(p, r, plan.g, i * kRows, kRows, lo, hi);
+            int32_t lo, hi, seen;
+            ragged_range<kUnit>(p, r, plan.g, i * kRows, kRows, lo, hi, seen);
             n += max(1, units_between<kUnit>(lo, hi)) + kRowPairCost;
         }
         return n;
@@ -311,7 +324,7 @@ __device__ __forceinline__ bool load_tile(const AttentionParams& p, const RowPla
         k.bidir = 0;
         k.own_len = lane < members ? own_length(p, c.seq + lane, bad) : 0;
         k.own_lo = own_first(p, m.prefix, k.own_len);
-        int32_t lo = lane < members ? prefix_first(p, m.prefix, k.own_len) : INT_MAX;
+        int32_t lo = lane < members ? prefix_seen(p, m.prefix, k.own_len) : INT_MAX;
         int32_t n = lane < members ? units_between<kUnit>(k.own_lo, k.own_len) : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -323,6 +336,8 @@ __device__ __forceinline__ bool load_tile(const AttentionParams& p, const RowPla
                 n += x;
         }
         k.own_end = n;
+        k.seen = lo;
+        lo &= ~(kUnit - 1);
         k.lo = lo;
         k.hi = m.prefix;
         k.prefix_units = plan.prefix_o ? 0 : units_between<kUnit>(lo, m.prefix);
@@ -338,7 +353,7 @@ __device__ __forceinline__ bool load_tile(const AttentionParams& p, const RowPla
         k.bidir = r.bidir;
         k.group = -1;
         k.own_len = k.own_lo = k.own_end = 0;
-        ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, k.lo, k.hi);
+        ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, k.lo, k.hi, k.seen);
         k.prefix_units = max(1, units_between<kUnit>(k.lo, k.hi));
         k.units = k.prefix_units;
         return true;
@@ -348,7 +363,8 @@ __device__ __forceinline__ bool load_tile(const AttentionParams& p, const RowPla
 // A warp's 16 keys of one unit.
 struct KeyBlock {
     const int32_t* table;
-    int32_t key0, end;  // keys [key0, min(key0 + 16, end)) of the table's positions
+    int32_t key0, end;  // keys [key0, min(key0 + 16, end)) of the table's positions,
+    int32_t seen;       // those before `seen` left out
     int32_t shift;      // position in the sequence = key + shift
     int32_t member;     // the only member whose rows see them; -1: all rows
 };
@@ -370,6 +386,7 @@ __device__ __forceinline__ KeyBlock key_block(const AttentionParams& p, const Cu
             b.table = p.block_table + (int64_t)(c.seq + member) * p.max_pages;
             b.key0 = lo + (u - (member > 0 ? before : 0)) * kUnit + warp * kBlock;
             b.end = member < k.ntok ? len : 0;
+            b.seen = own_seen(p, k.len, len);
             b.shift = k.len;
             b.member = member;
             return b;
@@ -380,6 +397,7 @@ __device__ __forceinline__ KeyBlock key_block(const AttentionParams& p, const Cu
     }
     b.key0 = k.lo + unit * kUnit + warp * kBlock;
     b.end = k.hi;
+    b.seen = k.seen;
     b.shift = 0;
     b.member = -1;
     return b;
@@ -390,7 +408,7 @@ __device__ __forceinline__ int64_t key_offset(const AttentionParams& p, const Ke
                                               int lane, bool& bad)
 {
     const int32_t key = b.key0 + (lane & (kBlock - 1));
-    if (key >= b.end)
+    if (key < b.seen || key >= b.end)
         return -1;
     int32_t pi, slot;
     split_position(p.map, key, pi, slot);
@@ -744,8 +762,8 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                 const Ragged r = load_ragged(p, s, ignore);
                 if (ragged_tiles(r, plan.g) > 1)
                     for (;; ++c.sub) {
-                        int32_t lo, hi;
-                        ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, lo, hi);
+                        int32_t lo, hi, seen;
+                        ragged_range<kUnit>(p, r, plan.g, c.sub * kRows, kRows, lo, hi, seen);
                         tile_line = max(1, units_between<kUnit>(lo, hi)) + kRowPairCost;
                         if (begin < (before + tile_line) * p.hk)
                             break;
@@ -1171,9 +1189,23 @@ size_t attention_counter_bytes()
     return kCounterBytes;
 }
 
-// Rows a sequence (or group) from which the tile kernel takes a call: below,
-// most of its 128-row tiles would be empty.
-constexpr int64_t kTileRowsFrom = 32;
+// Which calls go to the tile kernel, by their rows (tokens times query heads a
+// key head).  It takes ~35 us whatever it does and passes over the keys once for
+// up to 256 rows; the row kernel passes over them once for 16.
+//   Ragged batches (rows a sequence, row against tile kernel): 64 sequences on
+//   1,000 positions 16: 61 against 75 us, 24: 103 / 74, 64: 189 / 83; 8 on 4,000
+//   16: 38 / 47, 24: 54 / 47; 200 on 300 16: 73 / 86, 24: 115 / 87; but one on
+//   8,000 64: 34 / 36, 96: 39 / 37.
+//   Prefixes (rows a group): 8 groups on 2,000 positions 48: 64 / 66, 64: 79 / 71,
+//   128: 131 / 94; 20 on 500 64: 92 / 99, 128: 160 / 153; but one on 2,000 128:
+//   30 / 50.
+bool many_rows(const AttentionParams& p)
+{
+    const int64_t rows = p.tokens * (p.hq / p.hk);
+    if (p.group_start)
+        return rows >= 64 * (int64_t)p.n_groups && rows >= 512;
+    return rows > kRows * (int64_t)p.n_seqs && rows >= 96;
+}
 
 // The two kernels' partial results share a region: the second launch of a call
 // waits for the first.  The prefix's results of every (sequence, head) follow.
@@ -1181,7 +1213,7 @@ size_t attention_workspace_bytes(int64_t tokens, int hq, int head_dim)
 {
     const int dp = padded_head_dim(head_dim);
     size_t parts = (size_t)kMaxRowCtas * 2 * part_floats(dp) * sizeof(float);
-    if (dp > 128 || tokens * hq < kTileRowsFrom)
+    if (dp > 128 || tokens * hq < 96)  // too few rows for the tile kernel
         return kCounterBytes + parts;
     return kCounterBytes + std::max(parts, tile_part_bytes(dp)) +
            (size_t)tokens * hq * (dp + 2) * sizeof(float);
@@ -1205,12 +1237,10 @@ cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* 
     plan.tiles_a_seq = (int32_t)ceil_div(g, kRows);
     plan.min_units = kMinUnits;
 
-    // Many rows a key go to the tile kernel: all of a ragged batch, or the
-    // prefixes of a shared one (a window cuts prefixes row by row: the row
-    // kernel leaves out what nobody sees).
-    const int64_t entities = p.group_start ? p.n_groups : p.n_seqs;
-    if (p.tokens * g >= kTileRowsFrom * entities && tiles_can_run(p, dtype) &&
-        !(p.group_start && p.window > 0)) {
+    // The tile kernel takes all of a ragged batch, or the prefixes of a shared
+    // one (a window cuts prefixes row by row: the row kernel leaves out what
+    // nobody sees).
+    if (many_rows(p) && tiles_can_run(p, dtype) && !(p.group_start && p.window > 0)) {
         float* prefix_o = nullptr;
         float* prefix_ml = nullptr;
         if (p.group_start) {

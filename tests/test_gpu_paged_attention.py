@@ -8,7 +8,7 @@ import oracle
 import swiglu_ar_tts_b200 as ops
 from swiglu_ar_tts_b200 import inputs
 from gpu_util import dev, misaligned
-from paged_util import Batch, Groups, check_attention, score_constants
+from paged_util import UNUSED, Batch, Groups, check_attention, score_constants
 from tolerance import to_f64
 
 pytestmark = pytest.mark.gpu
@@ -50,6 +50,7 @@ MIXES = {
     "chunks": ([5, 17, 100], [300, 129, 411]),
     "more queries than keys": ([8, 20], [3, 0]),
     "long prompt": ([700], [700]),
+    "many more queries than keys": ([80, 70, 1], [3, 0, 200]),
     "prompt and steps": ([400, 1, 1, 1, 3], [400, 900, 33, 2, 65]),
 }
 
@@ -87,6 +88,8 @@ OPTIONS = {
     "bidirectional start": dict(bidir_lens=[0, 50, 10_000, 7]),
     "all": dict(softcap=20.0, window=100, slopes=True, bidir_lens=[3, 90, 1, 0]),
     "scale": dict(scale=-0.3),
+    "scale 0": dict(scale=0.0),
+    "tiny cap": dict(softcap=1e-20),
     "huge window": dict(window=2 ** 31 - 1),
 }
 
@@ -152,6 +155,74 @@ def test_strided_and_misaligned(dtype):
     assert torch.equal(run(b, q=q), want)
     check(b, run(b, q=misaligned(b.q)), "misaligned q")
     check(b, run(b, pools=(misaligned(b.k_pages), misaligned(b.v_pages))), "misaligned pages")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 70])
+def test_pages_in_front_of_a_window_may_be_gone(new, dtype):
+    """With a sliding window the table's first entries may lead nowhere."""
+    window = 100
+    b = Batch([new] * 2, [900, 1300], 16, 8, 128, 16, dtype, seed=23)
+    whole = b.table.copy()
+    got = run(b, window=window)
+    e = expected(b, window=window)
+    for s, n in enumerate(b.lens):
+        b.table[s, :(n - new - window + 1) // 16] = UNUSED
+    again = run(b, window=window)
+    assert ops.device_errors(clear=True) == 0
+    assert torch.equal(got, again)
+    check_attention(again, e, dtype, 200, "gone")
+    assert not np.array_equal(whole, b.table)
+
+
+def test_more_sequences_than_the_kernel_keeps_counts_of():
+    n = 9001
+    b = Batch([1] * n, [1 + i % 5 for i in range(n)], 2, 1, 64, 8, "bf16", seed=24)
+    check(b, run(b), "9001 sequences")
+
+
+def test_negative_lengths_are_empty():
+    b = Batch([1, 2, 60], [20, 0, 0], 16, 8, 128, 16, "bf16", seed=25)
+    b.kv_lens[1:] = [-5, -2 ** 31]
+    got = run(b)
+    assert not bool(got[1:63].any())
+
+
+@pytest.mark.parametrize("n", [1, 120])
+def test_dependent_launches(n):
+    """With programmatic dependent launch every kernel still waits for the one
+    before it: append, attention, append, attention without a pause."""
+    c = Batch([n], [n + 40], 16, 8, 128, 16, "bf16", seed=26)
+    start, lens, table = c.arrays()
+    k = inputs.normal((n, 8, 128), 27).cuda()
+    q, pos = dev(c.q), torch.zeros(3, n, dtype=torch.int32, device="cuda")
+    ws = ops.attention_prepare(torch.empty(ops.attention_workspace(n, 16, 128), dtype=torch.uint8,
+                                           device="cuda"))
+    results = []
+    for pdl in (False, True):
+        kp, vp = dev(c.k_pages), dev(c.v_pages)
+        out = [torch.empty_like(q) for _ in range(6)]
+        old = ops.set_pdl(pdl)
+        try:
+            torch.cuda._sleep(1_000_000)
+            for i in range(6):
+                ops.mrope_paged_append(q, k if i % 2 else -k, k if i % 2 else 2 * k, pos, start, lens, table,
+                                       kp, vp)
+                ops.paged_attention(q, kp, vp, start, lens, table, workspace=ws, out=out[i])
+        finally:
+            ops.set_pdl(old)
+        torch.cuda.synchronize()
+        results.append(torch.stack(out))
+    assert torch.equal(results[0], results[1])
+    assert torch.equal(results[0][0], results[0][2]) and not torch.equal(results[0][0], results[0][1])
+
+
+def test_workspace_that_was_not_cleared_is_flagged():
+    b = Batch([1], [20000], 16, 8, 128, 16, "bf16", seed=28)
+    ws = torch.full((ops.attention_workspace(1, 16, 128),), 0x11, dtype=torch.uint8, device="cuda")
+    ops.device_errors(clear=True)
+    run(b, workspace=ws)
+    assert ops.device_errors(clear=True) == 4  # AROPS_DEVICE_ERR_WORKSPACE
 
 
 def test_dense_cache_is_one_page_a_row():
@@ -301,6 +372,40 @@ def test_group_head_layouts(hq, hk, d, page, dtype):
                                   ([80], [260], [1 + 3 * i % 40 for i in range(80)])):
         b = Groups(members, prefix, lens, hq, hk, d, page, dtype, seed=31)
         shared_check(b, shared_run(b), f"{dtype} {hq}/{hk}/{d}/{page} {members}")
+
+
+# enough rows a group for the prefix to go to the tile kernel
+@pytest.mark.parametrize("hq,hk,d,page,members,prefix", [
+    (16, 8, 128, 16, [270], [500]), (16, 8, 128, 64, [150, 0, 128], [700, 9, 0]), (8, 1, 64, 32, [66], [129]),
+    (24, 3, 96, 24, [40, 40], [260, 1]), (40, 2, 80, 8, [30], [333]), (34, 1, 128, 16, [20], [128])])
+@pytest.mark.parametrize("opt", ["", "cap", "slopes", "all"])
+def test_groups_of_many_rows(hq, hk, d, page, members, prefix, opt):
+    o = {"": {}, "cap": dict(softcap=5.0), "slopes": dict(slopes=_slopes(hq)),
+         "all": dict(softcap=15.0, scale=-0.1, slopes=_slopes(hq))}[opt]
+    n, pad = sum(members), 3
+    b = Groups(members, prefix, [5 * i % 70 for i in range(n)] + [9] * pad, hq, hk, d, page, "bf16", seed=37,
+               pad=pad)
+    ws = ops.attention_prepare(torch.empty(ops.attention_workspace(n + pad, hq, d), dtype=torch.uint8,
+                                           device="cuda"))
+    got = shared_run(b, workspace=ws, **o)
+    shared_check(b, got, f"{hq}/{hk}/{d} {opt}", **o)
+    assert torch.equal(shared_run(b, workspace=ws, **o), got)
+
+
+def test_many_rows_bad_pages_and_lengths():
+    b = Groups([280], [400], [20] * 280, 16, 8, 128, 16, "bf16", seed=38)
+    b.prefix_table[0, 3] = -7
+    b.table[2, 1] = 1 << 30
+    b.prefix_lens[0] = 10 ** 6  # counts as the table's capacity
+    b.prefix_table = b.prefix_table[:, :25].copy()
+    ops.device_errors(clear=True)
+    got = shared_run(b)
+    assert ops.device_errors(clear=True) == 2
+    shared_check(b, got, "bad")
+    for start in ([0, 400], [-1, 280], [280, 0]):
+        b.group_start = np.array(start, dtype=np.int32)
+        assert bool((shared_run(b) == 7.0).all())
+        assert ops.device_errors(clear=True) == 2
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

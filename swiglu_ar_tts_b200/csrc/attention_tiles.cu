@@ -4,26 +4,40 @@
 //
 // The formula is the row kernel's.  A tile is 256 rows ((token, head of one
 // key/value head's group) pairs), two sub-tiles of 128, the M of tcgen05.mma; a
-// unit is 128 keys.  4 x 256 x 128 x 128 operations a unit are 2,048 clocks of
-// the SM's tensor cores, its 32,768 exponentials 2,048 clocks of its 16
-// exponential units a clock, its keys and values 64 KB: products and
-// exponentials bound it together, and all must run at once:
-//   warp 9  copies: keys and values of a unit by tensor maps, page by page, into
-//           a ring of slots in the 128-byte swizzle;
-//   warp 8  products: S_w = Q_w K^T into tensor memory, O_w += P_w V with P_w
-//           read from tensor memory, for the sub-tiles w in turn: P_0 V, the
-//           next S_0, P_1 V, the next S_1, so that one sub-tile's products run
-//           under the other's softmax;
-//   warps 0-3 and 4-7  softmax of sub-tiles 0 and 1, a row a thread: S out of
-//           tensor memory, maximum, exponentials, sum, P (bf16) back over S.
+// unit is 128 keys, taken in two halves of 64.  A unit's 4 x 256 x 128 x 128
+// operations are 2,048 clocks of the SM's tensor cores (2,624 with N = 64, where
+// shared memory feeds an M = 128 product at 50 clocks for 32: measured), its
+// 32,768 exponentials 2,048 clocks of the exponential units, its keys and values
+// 64 KB.  So everything runs at once, on sixteen warps:
+//   warp 9       copies: keys and values of a unit by tensor maps, page by page,
+//                into a ring of slots in the 128-byte swizzle;
+//   warp 10      the CTA's pieces of work (for all roles) and their queries;
+//   warps 8, 11  products of sub-tile 0 and 1: S_w = Q_w K^T into tensor memory,
+//                O_w += P_w V with P_w read from tensor memory;
+//   warps 0-3, 4-7    softmax of sub-tile 0 and 1, a row a thread: 64 scores out
+//                of tensor memory, maximum, exponentials, sum, P (bf16) back
+//                over them;
+//   warps 12-15  results: O out of tensor memory, divided by l, stored.
+// The two halves' scores lie in columns of their own: while a half is in the
+// softmax, the other half's weights are multiplied and its next scores made, so
+// the softmax warps never wait for products (traced: 150 clocks between a half's
+// end and the next one's first load, all of it the barrier's own latency).  A
+// unit takes 3,300 clocks, 62% of them exponentials: what is left between them
+// (maximum 200, loads and stores of tensor memory 140, barriers 250 of 1,650 a
+// half) is latency of the two warps that a scheduler has, and there is room for
+// no third in the registers.  Exponentials on the fp32 pipe (1/8 to 1/2 of them)
+// measured slower.  One prompt of 16,384 tokens, 16 heads on 8 of 128: 898 us,
+// 1,224 TFLOP/s (73% of the measured cuBLAS rate, 87% of its rate under the power
+// cap, which holds the clocks of repeated calls down: 910-1,000 us then).
+//
 // O stays in tensor memory; it is scaled only when a row's maximum has grown by
 // more than 2^8 since the last time (P and l carry the factor until then; both
 // are floating point, so nothing is lost).  Tensor memory: S_0, S_1, O_0, O_1,
 // all 512 columns, one CTA an SM.
 //
 // The line of units is cut into equal shares, as in the row kernel; partial
-// results go through the workspace and the last sub-tile to arrive joins them.
-// Every wait is bounded in time.
+// results go through the workspace and attention_join_kernel, launched behind,
+// joins them in the order of the keys.  Every wait is bounded in time.
 #include "attention_common.cuh"
 #include "tcgen05.cuh"
 

@@ -913,6 +913,13 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                     mma_bf16(s[1], a, kb[2], kb[3]);
                 }
             } else {
+                // the tensor cores cut every sum off instead of rounding it: the
+                // small products have a sum of their own, so that the large
+                // one is cut once a step
+                float rest[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    rest[t][0] = rest[t][1] = rest[t][2] = rest[t][3] = 0.0f;
 #pragma unroll 4
                 for (int step = 0; step < R::kSteps; ++step) {
                     const uint4* qf = reinterpret_cast<const uint4*>(qfrag) + (step * 32 + lane) * 2;
@@ -927,11 +934,16 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                                        ks + swizzled<T, DP>(row, step * 8 + quad)), h0, l0);
                         split_tf32(*reinterpret_cast<const float*>(
                                        ks + swizzled<T, DP>(row, step * 8 + 4 + quad)), h1, l1);
-                        mma_tf32(s[t], al, h0, h1);
-                        mma_tf32(s[t], ah, l0, l1);
+                        mma_tf32(rest[t], al, h0, h1);
+                        mma_tf32(rest[t], ah, l0, l1);
                         mma_tf32(s[t], ah, h0, h1);
                     }
                 }
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[t][e] += rest[t][e];
             }
 
             // softmax: what a row does not see is -inf
@@ -1010,7 +1022,9 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                     split_tf32(s[t][3], ah[t][3], al[t][3]);
                 }
 #pragma unroll
-                for (int n = 0; n < DP / 8; ++n)
+                for (int n = 0; n < DP / 8; ++n) {
+                    // these 16 keys' sum, then added to O with rounding
+                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const int row = t * 8 + 2 * quad;
@@ -1019,10 +1033,14 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                                        vs + swizzled<T, DP>(row, n * 8 + (lane >> 2))), h0, l0);
                         split_tf32(*reinterpret_cast<const float*>(
                                        vs + swizzled<T, DP>(row + 1, n * 8 + (lane >> 2))), h1, l1);
-                        mma_tf32(o[n], al[t], h0, h1);
-                        mma_tf32(o[n], ah[t], l0, l1);
-                        mma_tf32(o[n], ah[t], h0, h1);
+                        mma_tf32(add, al[t], h0, h1);
+                        mma_tf32(add, ah[t], l0, l1);
+                        mma_tf32(add, ah[t], h0, h1);
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[n][e] += add[e];
+                }
             }
             __syncwarp();  // every lane has read the stage that the next copy fills
             issue_next();

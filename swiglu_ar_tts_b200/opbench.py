@@ -2,6 +2,7 @@
 
     python -m swiglu_ar_tts_b200.opbench --op swiglu --iters 50
     python -m swiglu_ar_tts_b200.opbench --op all
+    python -m swiglu_ar_tts_b200.opbench --op paged_decode --rows 256
 
 Shapes are the operators' workload sizes (add+RMSNorm bf16 4096x2048, SwiGLU
 bf16 8192x6144, M-RoPE bf16 4096 tokens x 16/8 heads x 128, RMSNorm fp32
@@ -24,15 +25,17 @@ import statistics
 
 import torch
 
-from . import (add_layernorm, add_rmsnorm, layernorm, mrope_qk, rmsnorm, set_pdl, set_streaming,
-               set_topk_cluster, mrope_kv_append, swiglu, topk_sample, topk_sample_prepare,
-               topk_sample_workspace)
+from . import (add_layernorm, add_rmsnorm, attention_prepare, attention_workspace, layernorm,
+               mrope_paged_append, mrope_qk, paged_attention, rmsnorm, set_pdl, set_streaming,
+               set_topk_cluster, mrope_kv_append, shared_prefix_attention, swiglu, topk_sample,
+               topk_sample_prepare, topk_sample_workspace)
 from . import inputs as I
 from .chain import DecodeChain
 
 OPS = ("rmsnorm", "add_rmsnorm", "swiglu", "mrope_qk", "decode5", "decode256")
 EXTRA_OPS = ("layernorm", "add_layernorm", "decode5_ln", "decode256_ln", "topk_sample",
-             "mrope_kv_append", "copy_add_rmsnorm", "copy_mrope_qk", "copy_swiglu")
+             "mrope_kv_append", "mrope_paged_append", "paged_decode", "paged_prompt",
+             "shared_prefix", "copy_add_rmsnorm", "copy_mrope_qk", "copy_swiglu")
 # Size-matched device copies: a plain device-to-device copy (torch's copy
 # kernel, not this library's) that reads half and writes half of an
 # operator's algorithmic bytes at the workload size, as the ceiling a kernel
@@ -43,6 +46,27 @@ COPY_OF = {"copy_add_rmsnorm": (4 * 4096 * 2048 + 2048) * 2,
 
 
 CHAIN_PDL = True
+
+
+def _paged(rows: int, new: int, keys: int, dev: torch.device, seed: int, page: int = 16):
+    """A paged cache of the decoder's heads: `rows` sequences of `keys`
+    positions, the last `new` of them query tokens, pages in shuffled order."""
+    hq, hk, d = I.N_Q_HEADS, I.N_K_HEADS, I.HEAD_DIM
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    width = -(-keys // page)
+    table = torch.randperm(rows * width, generator=gen, device=dev).to(torch.int32).view(rows, width)
+    pools = [torch.empty(rows * width, hk, page, d, dtype=torch.bfloat16, device=dev)
+             .normal_(generator=gen) for _ in range(2)]
+    qkv = torch.empty(rows * new, (hq + 2 * hk) * d, dtype=torch.bfloat16, device=dev)
+    qkv.normal_(generator=gen)
+    return dict(
+        q=qkv[:, :hq * d].unflatten(1, (hq, d)), k=qkv[:, hq * d:(hq + hk) * d].unflatten(1, (hk, d)),
+        v=qkv[:, (hq + hk) * d:].unflatten(1, (hk, d)), k_pages=pools[0], v_pages=pools[1], table=table,
+        start=torch.arange(0, rows * new + 1, new, dtype=torch.int32, device=dev),
+        lens=torch.full((rows,), keys, dtype=torch.int32, device=dev),
+        out=torch.empty(rows * new, hq, d, dtype=torch.bfloat16, device=dev),
+        workspace=attention_prepare(torch.empty(attention_workspace(rows * new, hq, d),
+                                                dtype=torch.uint8, device=dev)))
 
 
 def make(op: str, rows: int | None, dev: torch.device, seed: int = 0):
@@ -103,6 +127,37 @@ def make(op: str, rows: int | None, dev: torch.device, seed: int = 0):
         nb = (2 * r * hq * d + 4 * r * hk * d) * 2 + 3 * r * 4 + 2 * r * 4
         return ((lambda: mrope_kv_append(q, k, v, pos, loc, kc, vc, I.SECTIONS, I.THETA, q_out=qo)),
                 nb, f"bf16 {r} tokens, cache [{cache_rows},{hk},{max_seq},{d}]")
+    if op == "mrope_paged_append":
+        r = rows or 4096
+        c = _paged(1, r, r, dev, seed) if r > 256 else _paged(r, 1, 512, dev, seed)
+        pos = I.mrope_positions(r).to(dev)
+        gamma = [I.normal((I.HEAD_DIM,), seed + 1 + i, mean=1.0, std=0.1).to(dev) for i in range(2)]
+        nb = r * ((2 * I.N_Q_HEADS + 4 * I.N_K_HEADS) * I.HEAD_DIM * 2 + 12)
+        return ((lambda: mrope_paged_append(c["q"], c["k"], c["v"], pos, c["start"], c["lens"],
+                                            c["table"], c["k_pages"], c["v_pages"], I.SECTIONS,
+                                            I.THETA, *gamma, q_out=c["out"])),
+                nb, f"bf16 {r} tokens, q/k norms, pages of 16")
+    if op in ("paged_decode", "paged_prompt"):
+        r = rows or (5 if op == "paged_decode" else 4096)
+        n, new, keys = (r, 1, 2000) if op == "paged_decode" else (1, r, r)
+        c = _paged(n, new, keys, dev, seed)
+        nb = n * (2 * new * I.N_Q_HEADS + 2 * keys * I.N_K_HEADS) * I.HEAD_DIM * 2
+        return ((lambda: paged_attention(c["q"], c["k_pages"], c["v_pages"], c["start"], c["lens"],
+                                         c["table"], workspace=c["workspace"], out=c["out"])),
+                nb, f"bf16 {n} sequences, {new} of {keys} positions new")
+    if op == "shared_prefix":
+        r = rows or 5
+        c, prefix = _paged(r, 1, 200, dev, seed), 2000
+        p = _paged(1, 1, prefix, dev, seed + 1)
+        shift = c["k_pages"].shape[0]  # one pool: the prefix's pages behind the sequences'
+        kp, vp = (torch.cat([c[x], p[x]]) for x in ("k_pages", "v_pages"))
+        group = torch.tensor([0, r], dtype=torch.int32, device=dev)
+        ptab = p["table"] + shift
+        nb = (2 * r * I.N_Q_HEADS + 2 * (prefix + r * 200) * I.N_K_HEADS) * I.HEAD_DIM * 2
+        return ((lambda: shared_prefix_attention(c["q"], kp, vp, group, p["lens"], ptab, c["lens"],
+                                                 c["table"], workspace=c["workspace"],
+                                                 out=c["out"])),
+                nb, f"bf16 {r} candidates of 200 positions on a prompt of {prefix}")
     if op == "topk_sample":
         r = rows or 5
         t = {k: v.to(dev) for k, v in I.topk_inputs(r, 151936, 50, "bf16", seed).items()}

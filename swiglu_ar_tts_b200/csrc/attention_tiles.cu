@@ -674,7 +674,9 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const Score
     auto both = [](float x) { return make_float2(x, x); };
     const float out = map.scale * kLog2e;
     const float bias = -slope * kLog2e;
-    const float2 step = both(-bias), first = both(bias * (float)gap);
+    // the bias of keys e, e + 1 (e = 0, 2, .. 14); of those 16, 32, 48 on: one
+    // more addition each
+    const float2 step = both(-16.0f * bias);
     const bool behind = __any_sync(0xFFFFFFFFu, gap < kHalfUnit - 1);
     if (map.cap > 0.0f) {
         float big = 0.0f;
@@ -687,20 +689,27 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const Score
             const float2 c0 = both(kTanh0 * out), c1 = both(kTanh1 * out * in2),
                          c2 = both(kTanh2 * out * (in2 * in2)),
                          c3 = both(kTanh3 * out * (in2 * in2 * in2));
+            if (behind) {
 #pragma unroll
-            for (int i = 0; i < kHalfUnit; i += 2) {
-                const float2 x = at(i);
-                const float2 y = mul2(x, x);
-                float2 q = fma2(y, c3, c2);
-                q = fma2(q, y, c1);
-                q = fma2(q, y, c0);
-                if (behind)
-                    put(i, mul2(x, q));
-                else
-                    put(i, fma2(x, q, fma2(step, make_float2((float)i, (float)(i + 1)), first)));
-            }
-            if (!behind)
+                for (int i = 0; i < kHalfUnit; i += 2) {
+                    const float2 x = at(i);
+                    const float2 y = mul2(x, x);
+                    put(i, mul2(x, fma2(fma2(fma2(y, c3, c2), y, c1), y, c0)));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    float2 add = make_float2(bias * (float)(gap - e), bias * (float)(gap - e - 1));
+#pragma unroll
+                    for (int i = e; i < kHalfUnit; i += 16) {
+                        const float2 x = at(i);
+                        const float2 y = mul2(x, x);
+                        put(i, fma2(x, fma2(fma2(fma2(y, c3, c2), y, c1), y, c0), add));
+                        add = add2(add, step);
+                    }
+                }
                 return;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < kHalfUnit; ++i)

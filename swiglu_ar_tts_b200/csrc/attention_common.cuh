@@ -8,10 +8,9 @@ namespace arops {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The workspace: 16 KiB of arrival counters (zero between calls), 2048 for the
-// row kernel and 2048 for the tile kernel, then their partial results.
+// The workspace: 16 KiB of the row kernel's arrival counters (one a CTA, zero
+// between calls), then partial results.
 constexpr int kCounterBytes = 16384;
-constexpr int kMaxAttentionCtas = 2048;
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -25,6 +24,15 @@ __device__ __forceinline__ float reciprocal_fast(float x)
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// What a partial result with maximum m_x is multiplied by when the joined
+// maximum is m: 2^(m_x - m), and 0 if m_x is -inf.  Such a part's O and l are
+// multiplied by the 0, not left out: where all scores are NaN the maximum stays
+// -inf, and the row keeps its NaN.
+__device__ __forceinline__ float part_factor(float mx, float m)
+{
+    return mx == -INFINITY ? 0.0f : exp2_fast(mx - m);
 }
 
 // s / cap through tanh, times cap: tanh(x) = 1 - 2 / (1 + e^2x).  Its absolute

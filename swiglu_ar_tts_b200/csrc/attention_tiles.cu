@@ -1076,8 +1076,8 @@ attention_join_kernel(const __grid_constant__ AttentionParams p,
         for (int e = 0; e < 8; ++e)
             v[e] = *reinterpret_cast<const float4*>(src + ((col / 4 + e) * kSubRows + tid) * 4);
         const float mn = fmaxf(m, mx);
-        const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
-        const float fx = mx == -INFINITY ? 0.0f : exp2_fast(mx - mn);
+        const float f = part_factor(m, mn);
+        const float fx = part_factor(mx, mn);
         m = mn;
         l = l * f + lx * fx;
 #pragma unroll

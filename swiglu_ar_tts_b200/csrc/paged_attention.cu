@@ -530,7 +530,7 @@ __device__ __forceinline__ void store_group(__nv_bfloat16* dst, const float* f, 
 }
 
 // Four values of a row: the prefix's part joined, divided by l, stored.  A row
-// that sees no key has l == 0 and gets zeros; one that met a NaN keeps it.
+// that sees no key has l == 0 and gets zeros.
 template <typename T, int DP, bool SHARED>
 __device__ __forceinline__ void store_result(const AttentionParams& p, const RowPlan& plan,
                                              const RowOf& r, int e, float* sum, float m, float l)
@@ -539,16 +539,14 @@ __device__ __forceinline__ void store_result(const AttentionParams& p, const Row
     if (SHARED && plan.prefix_o) {
         const float2 ml = __ldcg(reinterpret_cast<const float2*>(plan.prefix_ml) + row);
         const float4 o = __ldcg(reinterpret_cast<const float4*>(plan.prefix_o + row * DP + e));
-        if (ml.x != -INFINITY) {
-            const float mm = fmaxf(m, ml.x);
-            const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mm);
-            const float fp = exp2_fast(ml.x - mm);
-            l = l * f + ml.y * fp;
-            sum[0] = sum[0] * f + o.x * fp;
-            sum[1] = sum[1] * f + o.y * fp;
-            sum[2] = sum[2] * f + o.z * fp;
-            sum[3] = sum[3] * f + o.w * fp;
-        }
+        const float mm = fmaxf(m, ml.x);
+        const float f = part_factor(m, mm);
+        const float fp = part_factor(ml.x, mm);
+        l = l * f + ml.y * fp;
+        sum[0] = sum[0] * f + o.x * fp;
+        sum[1] = sum[1] * f + o.y * fp;
+        sum[2] = sum[2] * f + o.z * fp;
+        sum[3] = sum[3] * f + o.w * fp;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -585,8 +583,7 @@ __device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const 
         if (few)
             weights[(x - cta0) * kRows + row] = mx;
         const float mn = fmaxf(m, mx);
-        if (mx != -INFINITY)
-            l = (m == -INFINITY ? 0.0f : l * exp2_fast(m - mn)) + lx * exp2_fast(mx - mn);
+        l = l * part_factor(m, mn) + lx * part_factor(mx, mn);
         m = mn;
     }
     float* lead_m = weights + kMost * kRows;
@@ -602,17 +599,14 @@ __device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const 
             m = fmaxf(m, lead_m[i * kRows + row]);
 #pragma unroll
         for (int i = 0; i < kLeads; ++i)
-            if (lead_m[i * kRows + row] != -INFINITY)
-                l += lead_l[i * kRows + row] * exp2_fast(lead_m[i * kRows + row] - m);
+            l += lead_l[i * kRows + row] * part_factor(lead_m[i * kRows + row], m);
         row_m[0][row] = m;
         row_l[0][row] = l;
     }
     __syncthreads();
     if (few)
-        for (int i = threadIdx.x; i < (cta1 - cta0 + 1) * kRows; i += kRowThreads) {
-            const float mx = weights[i];
-            weights[i] = mx == -INFINITY ? 0.0f : exp2_fast(mx - row_m[0][i % kRows]);
-        }
+        for (int i = threadIdx.x; i < (cta1 - cta0 + 1) * kRows; i += kRowThreads)
+            weights[i] = part_factor(weights[i], row_m[0][i % kRows]);
     __syncthreads();
 #pragma unroll 1
     for (int idx = threadIdx.x; idx < kRows * DP / 4; idx += kRowThreads) {
@@ -636,7 +630,7 @@ __device__ void join_parts(const AttentionParams& p, const RowPlan& plan, const 
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (!few)
-                    f[j] = f[j] == -INFINITY ? 0.0f : exp2_fast(f[j] - row_m[0][at]);
+                    f[j] = part_factor(f[j], row_m[0][at]);
                 if (x + j > cta1)
                     f[j] = 0.0f;
                 sum[0] = fmaf(v[j].x, f[j], sum[0]);
@@ -1068,7 +1062,7 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
 #pragma unroll
             for (int w = 0; w < kRowWarps; ++w)
                 mm = fmaxf(mm, row_m[w][row]);
-            const float f = m[i] == -INFINITY ? 0.0f : exp2_fast(m[i] - mm);
+            const float f = part_factor(m[i], mm);
             if (row_at[row].token < 0)
                 continue;
             float* dst = joined + (warp * kRows + row) * DP + 2 * quad;
@@ -1102,8 +1096,7 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                 sum[1] += x.y;
                 sum[2] += x.z;
                 sum[3] += x.w;
-                if (row_m[w][row] != -INFINITY)
-                    ll += row_l[w][row] * exp2_fast(row_m[w][row] - mm);
+                ll += row_l[w][row] * part_factor(row_m[w][row], mm);
             }
             if (whole) {
                 if (e >= p.head_dim)

@@ -225,6 +225,23 @@ def test_workspace_that_was_not_cleared_is_flagged():
     assert ops.device_errors(clear=True) == 4  # AROPS_DEVICE_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("opt", [{}, {"softcap": 5.0}])
+@pytest.mark.parametrize("new,lens", [([1, 1, 1], [1, 40, 900]), ([1], [9000]), ([3, 40], [3, 70]),
+                                      ([130, 60], [130, 200]), ([40], [6000])])
+def test_nan_query_row_stays_nan(new, lens, opt, dtype):
+    """All of a NaN query's scores are NaN: whichever parts its row is joined
+    from, it is not an empty row.  Other rows are what they were."""
+    b = Batch(new, lens, 16, 8, 128, 16, dtype, seed=81)
+    q = dev(b.q).clone()
+    t, h = b.tokens - 1, 5
+    q[t, h, 3] = float("nan")
+    got = run(b, q=q, **opt)
+    assert bool(torch.isnan(got[t, h]).all())
+    got[t, h] = torch.from_numpy(expected(b, **opt)[0][t, h]).to(got)
+    check(b, got, f"nan {new}", **opt)
+
+
 def test_dense_cache_is_one_page_a_row():
     """The dense cache of mrope_kv_append: rows are pages, the table the identity."""
     b = Batch([1] * 4, [300, 20, 1, 299], 16, 8, 128, 300, "bf16", seed=16, spare=0)
@@ -461,6 +478,20 @@ def test_group_bad_pages_are_flagged():
         got = shared_run(b)
         assert ops.device_errors(clear=True) == 2
         shared_check(b, got, f"bad {members}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("members,prefix,own", [([5], [300], 20), ([80], [300], 20), ([80], [300], 0),
+                                                ([300], [4000], 70)])
+def test_nan_query_of_a_group_stays_nan(members, prefix, own, dtype):
+    b = Groups(members, prefix, [own] * sum(members), 16, 8, 128, 16, dtype, seed=83)
+    q = dev(b.q).clone()
+    t, h = b.n - 2, 9
+    q[t, h, 100] = float("nan")
+    got = shared_run(b, q=q)
+    assert bool(torch.isnan(got[t, h]).all())
+    got[t, h] = torch.from_numpy(shared_expected(b)[0][t, h]).to(got)
+    shared_check(b, got, f"nan {members}")
 
 
 def test_malformed_groups_stay_in_bounds():

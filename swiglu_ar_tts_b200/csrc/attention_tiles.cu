@@ -257,7 +257,7 @@ struct TileShared {
     uint64_t empty[TileTraits<DP>::kSlots];
     uint64_t piece_full[kPieces];
     uint64_t piece_empty[kPieces];
-    uint64_t tail;        // a copy of values that reaches past the sequence's end
+    uint64_t tail;        // a copy that reaches past the sequence's end
     uint64_t q_ready[2];
     uint64_t q_free[2];   // a piece's last product with Q_w is done
     uint64_t s_full[2][2];   // [sub-tile][half]
@@ -372,7 +372,7 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                 if (!ok)
                     break;
                 unsigned char* dst = slots + s * R::kSlot;
-                const bool clean = kv == 1 && tail;
+                const bool clean = tail && (kv == 1 || p.softcap > 0.0f);
                 const uint32_t bar = smem_addr(clean ? &sh.tail : &sh.full[s]);
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar, R::kSlot);
@@ -386,7 +386,9 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                 ++n;
                 if (clean) {
                     // slots behind the sequence's end may hold anything, and 0
-                    // times a NaN is one: their values become zeros
+                    // times a NaN is one: their values become zeros.  With a cap
+                    // their keys do too: a warp takes the form of tanh that all
+                    // of its products allow, those of masked keys among them.
                     ok = warp_wait(&sh.tail, tails & 1, &sh.stop, p.err);
                     ++tails;
                     if (!ok)
@@ -766,10 +768,10 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                                         p.max_pages * p.map.page_size, ignore);
             } else {
                 pos = t.len - t.ntok + (int32_t)r.tok;
+                // (nobody reads a row that does not exist, but it has a vote in
+                // the scaling of its warp's sums: no keys behind the length)
                 if (valid)
                     visible_keys(pos, t.len, t.bidir, p.window, lo, hi);
-                else
-                    hi = INT_MAX;  // nobody reads such a row
             }
             if (FULL && p.slopes && valid)
                 slope = __ldg(p.slopes + t.kvh * plan.g.n + r.head);

@@ -242,6 +242,17 @@ def test_nan_query_row_stays_nan(new, lens, opt, dtype):
     check(b, got, f"nan {new}", **opt)
 
 
+@pytest.mark.parametrize("new,lens", [([1, 1], [30, 700]), ([100, 30], [100, 230]), ([7, 60], [1000, 99])])
+@pytest.mark.parametrize("opt", [{}, {"softcap": 20.0}, {"softcap": 3.0, "slopes": _slopes(16)}])
+def test_what_lies_behind_a_length_changes_no_bit(new, lens, opt):
+    b = Batch(new, lens, 16, 8, 128, 16, "bf16", seed=85)
+    first = run(b, **opt)
+    check(b, first, "NaN behind", **opt)
+    for value in (0.0, 3e4, float("inf")):
+        pools = [dev(torch.nan_to_num(x, nan=value)) for x in (b.k_pages, b.v_pages)]
+        assert torch.equal(run(b, pools=pools, **opt), first), f"{value} behind"
+
+
 def test_dense_cache_is_one_page_a_row():
     """The dense cache of mrope_kv_append: rows are pages, the table the identity."""
     b = Batch([1] * 4, [300, 20, 1, 299], 16, 8, 128, 300, "bf16", seed=16, spare=0)
@@ -492,6 +503,16 @@ def test_nan_query_of_a_group_stays_nan(members, prefix, own, dtype):
     assert bool(torch.isnan(got[t, h]).all())
     got[t, h] = torch.from_numpy(shared_expected(b)[0][t, h]).to(got)
     shared_check(b, got, f"nan {members}")
+
+
+@pytest.mark.parametrize("members,prefix", [([5], [300]), ([80], [300])])
+@pytest.mark.parametrize("opt", [{}, {"softcap": 20.0}])
+def test_what_lies_behind_a_prefix_changes_no_bit(members, prefix, opt):
+    b = Groups(members, prefix, [20] * sum(members), 16, 8, 128, 16, "bf16", seed=86)
+    first = shared_run(b, **opt)
+    for value in (0.0, 3e4, float("inf")):
+        pools = [dev(torch.nan_to_num(x, nan=value)) for x in (b.k_pages, b.v_pages)]
+        assert torch.equal(shared_run(b, pools=pools, **opt), first), f"{value} behind"
 
 
 def test_malformed_groups_stay_in_bounds():

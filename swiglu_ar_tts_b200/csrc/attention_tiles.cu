@@ -1408,10 +1408,16 @@ cudaError_t launch_tiles_d(const AttentionParams& p, const TilePlan& plan, const
 
 }  // namespace
 
+// Waits are bounded by a second, and some last as long as a CTA is at one or two
+// tiles: 2^23 positions are at most 65,536 units of 2 to 4 us each.  Calls whose
+// tables hold more go to the row kernel, which waits for nobody.
+constexpr int64_t kMaxTilePositions = 1 << 23;
+
 bool tiles_can_run(const AttentionParams& p, arops_dtype dtype)
 {
+    const int64_t pages = p.group_start ? p.max_prefix_pages : p.max_pages;
     return dtype == AROPS_BF16 && p.head_dim <= 128 && p.head_dim % 8 == 0 &&
-           p.map.page_size % 8 == 0 && aligned16(p.k_pages) && aligned16(p.v_pages) &&
+           pages * p.map.page_size <= kMaxTilePositions && p.map.page_size % 8 == 0 && aligned16(p.k_pages) && aligned16(p.v_pages) &&
            aligned16(p.q) && p.q_stride % 8 == 0 && aligned16(p.out) &&
            // the tensor map's largest stride
            (int64_t)p.hk * p.map.page_size * p.head_dim * 2 < (1ll << 40);

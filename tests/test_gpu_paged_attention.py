@@ -253,6 +253,16 @@ def test_what_lies_behind_a_length_changes_no_bit(new, lens, opt):
         assert torch.equal(run(b, pools=pools, **opt), first), f"{value} behind"
 
 
+def test_very_wide_tables():
+    """Tables for more positions than the tile kernel takes, and one for exactly as many."""
+    for pages in (2 ** 16, 2 ** 16 + 1):
+        b = Batch([100, 30], [300, 30], 16, 8, 128, 128, "bf16", seed=87)
+        wide = np.full((2, pages), UNUSED, dtype=np.int32)
+        wide[:, :b.table.shape[1]] = b.table
+        b.table = wide
+        check(b, run(b), f"{pages} pages")
+
+
 def test_dense_cache_is_one_page_a_row():
     """The dense cache of mrope_kv_append: rows are pages, the table the identity."""
     b = Batch([1] * 4, [300, 20, 1, 299], 16, 8, 128, 300, "bf16", seed=16, spare=0)

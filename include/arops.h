@@ -296,7 +296,7 @@ typedef struct {
  *               of one stream may.
  * The work (all keys of all rows) is cut into equal shares, one a CTA, from the
  * lengths on the device: no host plan, no dependence on the order of arrival,
- * and the same lengths give the same bits.
+ * and the same lengths give the same bits.  A call enqueues one to three kernels.
  */
 AROPS_API arops_status arops_attention_workspace(int64_t tokens, int32_t n_q_heads,
                                                  int32_t head_dim, size_t* bytes);

@@ -26,9 +26,10 @@
 // (maximum 200, loads and stores of tensor memory 140, barriers 250 of 1,650 a
 // half) is latency of the two warps that a scheduler has, and there is room for
 // no third in the registers.  Exponentials on the fp32 pipe (1/8 to 1/2 of them)
-// measured slower.  One prompt of 16,384 tokens, 16 heads on 8 of 128: 898 us,
-// 1,224 TFLOP/s (73% of the measured cuBLAS rate, 87% of its rate under the power
-// cap, which holds the clocks of repeated calls down: 910-1,000 us then).
+// measured slower, and so did weights taken with the maximum before this half's.
+// One prompt of 16,384 tokens, 16 heads on 8 of 128: 886 us, 1,241 TFLOP/s (74% of
+// the measured cuBLAS rate, 88% of its rate under the power cap, which holds the
+// clocks of repeated calls down: 900-1,040 us then).
 //
 // O stays in tensor memory; it is scaled only when a row's maximum has grown by
 // more than 2^8 since the last time (P and l carry the factor until then; both
@@ -1417,7 +1418,8 @@ bool tiles_can_run(const AttentionParams& p, arops_dtype dtype)
 {
     const int64_t pages = p.group_start ? p.max_prefix_pages : p.max_pages;
     return dtype == AROPS_BF16 && p.head_dim <= 128 && p.head_dim % 8 == 0 &&
-           pages * p.map.page_size <= kMaxTilePositions && p.map.page_size % 8 == 0 && aligned16(p.k_pages) && aligned16(p.v_pages) &&
+           pages * p.map.page_size <= kMaxTilePositions && p.map.page_size % 8 == 0 &&
+           aligned16(p.k_pages) && aligned16(p.v_pages) &&
            aligned16(p.q) && p.q_stride % 8 == 0 && aligned16(p.out) &&
            // the tensor map's largest stride
            (int64_t)p.hk * p.map.page_size * p.head_dim * 2 < (1ll << 40);

@@ -11,8 +11,8 @@
 // decode step is bound by latency: positions, lengths and the block table form
 // a chain of three dependent loads, the activations' loads run beside it (5
 // tokens: 3.3 us a launch back to back).  A ragged batch of 7,443 tokens, 122 MB,
-// takes 29.3 us, 64% of the measured copy rate: 950 instructions a warp and half
-// token (angles, norms, rotation) keep 41% of the issue slots busy, and an SM's
+// takes 28.0 us, 66% of the measured copy rate: 950 instructions a warp and half
+// token (angles, norms, rotation) keep half of the issue slots busy, and an SM's
 // sixteen warps do not cover the rest of each other's latencies; more warps of
 // fewer registers, weights kept in registers, or the next token's data brought
 // into L2 ahead measured the same or slower.

@@ -78,7 +78,7 @@ __device__ __forceinline__ void tc_commit(uint32_t bar)
         : "memory");
 }
 
-__device__ __forceinline__ void tc_fence_before() 
+__device__ __forceinline__ void tc_fence_before()
 {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }

@@ -73,6 +73,16 @@ def test_head_layouts_and_pages(hq, hk, d, page, dtype):
         check(b, run(b), f"{dtype} {hq}/{hk}/{d}/{page} {new}")
 
 
+@pytest.mark.parametrize("hq,hk,d,page", [(128, 1, 64, 16), (256, 2, 16, 8), (48, 1, 120, 16), (5, 1, 24, 40),
+                                          (260, 1, 72, 256)])
+def test_tile_kernel_heads(hq, hk, d, page):
+    """Heads a token that fill, divide and outnumber the rows of a tile; narrow ones."""
+    b = Batch([3, 40, 0, 1], [100, 290, 7, 140], hq, hk, d, page, "bf16", seed=hq + d, pad=1)
+    check(b, run(b), f"{hq}/{hk}/{d}/{page}")
+    opt = dict(softcap=4.0, slopes=_slopes(hq), window=90)
+    check(b, run(b, **opt), f"{hq}/{hk}/{d}/{page} options", **opt)
+
+
 @pytest.mark.parametrize("d", [136, 192, 255, 256])
 def test_wide_heads(d):
     for new, lens in (([1, 1, 4], [200, 33, 77]), ([60, 2], [90, 301])):

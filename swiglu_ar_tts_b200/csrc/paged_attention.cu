@@ -96,11 +96,15 @@ __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// x as the sum of two tf32 numbers (11 significant bits each): 2^-22 of x is left out.
+// x as the sum of two tf32 numbers (11 significant bits each), by integer
+// operations: conversions run at an eighth of their rate.  The first is rounded
+// (half away from zero, as a conversion would); what is left, 12 bits and exact,
+// is cut to 11: 2^-23 of x is left out.  A NaN whose first part the rounding
+// carries into the sign is one in the second.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo)
 {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr)

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -65,6 +66,17 @@ class _PrefixGroups(ctypes.Structure):
                 ("n_groups", _i32), ("max_prefix_pages", _i32)]
 
 
+# The same structures as bytes.  The tensor wrappers pass these: packing is a
+# quarter of the cost of a Structure, and refuses a number that a field cannot
+# hold where a Structure would cut it to the field's bits.
+_pack_cache = struct.Struct("@PPqiiii").pack
+_pack_batch = struct.Struct("@PPPii").pack
+_pack_options = struct.Struct("@ffiPP").pack
+_pack_groups = struct.Struct("@PPPii").pack
+_Sections = _i32 * 3
+_append_call = _attention_call = _shared_call = None  # set by lib()
+
+
 class ArOpsError(RuntimeError):
     """A non-OK status from libarops; ``status`` holds the code."""
 
@@ -79,7 +91,7 @@ def lib_path() -> str:
 
 def lib() -> ctypes.CDLL:
     """The loaded libarops.so (loaded on first use; raises if it is missing)."""
-    global _lib
+    global _lib, _append_call, _attention_call, _shared_call
     if _lib is not None:
         return _lib
     with _lock:
@@ -128,6 +140,18 @@ def lib() -> ctypes.CDLL:
                    "arops_attention_prepare", "arops_paged_attention",
                    "arops_shared_prefix_attention"):
             getattr(L, fn).restype = ctypes.c_int
+        packed = {cache: ctypes.c_char_p, batch: ctypes.c_char_p, options: ctypes.c_char_p,
+                  groups: ctypes.c_char_p}
+
+        def with_bytes(name):
+            fn = L[name]  # a function object of its own
+            fn.argtypes = [packed.get(t, t) for t in getattr(L, name).argtypes]
+            fn.restype = ctypes.c_int
+            return fn
+
+        _append_call = with_bytes("arops_mrope_paged_append")
+        _attention_call = with_bytes("arops_paged_attention")
+        _shared_call = with_bytes("arops_shared_prefix_attention")
         L.arops_set_pdl.argtypes = [ctypes.c_int]
         L.arops_set_pdl.restype = ctypes.c_int
         L.arops_set_streaming.argtypes = [ctypes.c_int]
@@ -373,6 +397,13 @@ def _need(name: str, t: torch.Tensor, device: int, dtype: torch.dtype, shape) ->
         _reject(name, t, device, dtype, shape)
 
 
+def _pack(pack, *values) -> bytes:
+    try:
+        return pack(*values)
+    except (struct.error, OverflowError, TypeError) as e:
+        raise ValueError(f"an argument is not of its type or range: {e}") from None
+
+
 def _token_stride(name: str, t: torch.Tensor) -> int:
     """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
     heads are dense (a slice of a packed projection is)."""
@@ -390,7 +421,8 @@ def _token_stride(name: str, t: torch.Tensor) -> int:
 
 
 def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, device: int, dtype: torch.dtype,
-          head_dim: int) -> _PagedCache:
+          head_dim: int) -> tuple[bytes, int]:
+    """arops_paged_cache of the two pools, and their heads."""
     code = DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}; use torch.float32 or torch.bfloat16")
@@ -401,7 +433,7 @@ def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, device: int, dtype: torc
         raise ValueError(f"the pages hold heads of {d}, q heads of {head_dim}")
     _need("k_pages", k_pages, device, dtype, None)
     _need("v_pages", v_pages, device, dtype, k_pages.shape)
-    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, page, hk, d, code)
+    return _pack(_pack_cache, k_pages.data_ptr(), v_pages.data_ptr(), n, page, hk, d, code), hk
 
 
 def _table(name: str, t: torch.Tensor, device: int, rows: int) -> int:
@@ -435,8 +467,8 @@ def mrope_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: t
         so = _token_stride("q_out", q_out)
         if q_out.get_device() != device or q_out.dtype != dtype or q_out.shape != q.shape:
             _reject("q_out", q_out, device, dtype, q.shape)
-    cache = _pool(k_pages, v_pages, device, dtype, d)
-    shape = (tokens, cache.n_kv_heads, d)
+    cache, hk = _pool(k_pages, v_pages, device, dtype, d)
+    shape = (tokens, hk, d)
     if k.get_device() != device or k.dtype != dtype or k.shape != shape:
         _reject("k", k, device, dtype, shape)
     if v.get_device() != device or v.dtype != dtype or v.shape != shape:
@@ -454,10 +486,12 @@ def mrope_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: t
     _need("q_start", q_start, device, i32, (n + 1,))
     _need("kv_lens", kv_lens, device, i32, (n,))
     pages = _table("block_table", block_table, device, n)
-    batch = _PagedBatch(q_start.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, pages)
-    _launch(device, lib().arops_mrope_paged_append, q.data_ptr(), sq, k.data_ptr(), sk,
-            v.data_ptr(), sv, q_out.data_ptr(), so, cache, batch, gq, gk, eps, pos.data_ptr(),
-            tokens, hq, (_i32 * 3)(*sections), theta)
+    batch = _pack(_pack_batch, q_start.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n,
+                  pages)
+    lib()
+    _launch(device, _append_call, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
+            q_out.data_ptr(), so, cache, batch, gq, gk, eps, pos.data_ptr(), tokens, hq,
+            _Sections(*sections), theta)
     return q_out
 
 
@@ -480,13 +514,14 @@ def attention_prepare(workspace: torch.Tensor) -> torch.Tensor:
     return workspace
 
 
-def _attention_args(q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes,
-                    bidir_lens, workspace, out):
-    """Checks and arguments that both attention operators share."""
+def _attention_args(q, k_pages, v_pages, q_start, kv_lens, block_table, scale, softcap, window,
+                    slopes, bidir_lens, workspace, out):
+    """Checks and arguments that both attention operators share (q_start: None
+    where every sequence has one token)."""
     device, dtype = _device_of("q", q), q.dtype
     stride = _token_stride("q", q)
     tokens, hq, d = q.shape
-    cache = _pool(k_pages, v_pages, device, dtype, d)
+    cache, _ = _pool(k_pages, v_pages, device, dtype, d)
     if out is None:
         out = torch.empty(tokens, hq, d, dtype=dtype, device=q.device)
     else:
@@ -494,19 +529,25 @@ def _attention_args(q, k_pages, v_pages, kv_lens, block_table, scale, softcap, w
     n = kv_lens.numel()
     _need("kv_lens", kv_lens, device, torch.int32, (n,))
     pages = _table("block_table", block_table, device, n)
-    options = _AttentionOptions(d ** -0.5 if scale is None else scale, softcap, window, None, None)
+    starts = slope_ptr = bidir_ptr = 0
+    if q_start is not None:
+        _need("q_start", q_start, device, torch.int32, (n + 1,))
+        starts = q_start.data_ptr()
     if slopes is not None:
         _need("slopes", slopes, device, torch.float32, (hq,))
-        options.slopes = slopes.data_ptr()
+        slope_ptr = slopes.data_ptr()
     if bidir_lens is not None:
         _need("bidir_lens", bidir_lens, device, torch.int32, (n,))
-        options.bidir_lens = bidir_lens.data_ptr()
+        bidir_ptr = bidir_lens.data_ptr()
+    options = _pack(_pack_options, d ** -0.5 if scale is None else scale, softcap, window,
+                    slope_ptr, bidir_ptr)
+    batch = _pack(_pack_batch, starts, kv_lens.data_ptr(), block_table.data_ptr(), n, pages)
     if workspace is None:
         workspace = attention_prepare(torch.empty(attention_workspace(tokens, hq, d),
                                                   dtype=torch.uint8, device=q.device))
     elif workspace.get_device() != device or not workspace.is_contiguous():
         _reject("workspace", workspace, device, workspace.dtype, None)
-    batch = _PagedBatch(None, kv_lens.data_ptr(), block_table.data_ptr(), n, pages)
+    lib()
     return device, stride, cache, batch, options, workspace, out
 
 
@@ -526,12 +567,11 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     uint8 tensor of attention_workspace() bytes, cleared once
     (attention_prepare); allocated and cleared here if omitted."""
     device, stride, cache, batch, options, workspace, out = _attention_args(
-        q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes, bidir_lens,
-        workspace, out)
-    _need("q_start", q_start, device, torch.int32, (batch.n_seqs + 1,))
-    batch.q_start = q_start.data_ptr()
-    _launch(device, lib().arops_paged_attention, q.data_ptr(), stride, out.data_ptr(), cache,
-            batch, options, q.shape[0], q.shape[1], workspace.data_ptr(), workspace.nbytes)
+        q, k_pages, v_pages, q_start, kv_lens, block_table, scale, softcap, window, slopes,
+        bidir_lens, workspace, out)
+    tokens, hq, _ = q.shape
+    _launch(device, _attention_call, q.data_ptr(), stride, out.data_ptr(), cache, batch, options,
+            tokens, hq, workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -549,18 +589,18 @@ def shared_prefix_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     kv_lens[s] positions (pages block_table[s]), at whose end it stands.
     Options, workspace and ``out`` as for paged_attention."""
     device, stride, cache, batch, options, workspace, out = _attention_args(
-        q, k_pages, v_pages, kv_lens, block_table, scale, softcap, window, slopes, None,
+        q, k_pages, v_pages, None, kv_lens, block_table, scale, softcap, window, slopes, None,
         workspace, out)
-    if q.shape[0] != batch.n_seqs:
+    if q.shape[0] != kv_lens.numel():
         raise ValueError("q must hold one token per sequence")
     n = prefix_lens.numel()
     _need("group_start", group_start, device, torch.int32, (n + 1,))
     _need("prefix_lens", prefix_lens, device, torch.int32, (n,))
     pages = _table("prefix_table", prefix_table, device, n)
-    groups = _PrefixGroups(group_start.data_ptr(), prefix_lens.data_ptr(), prefix_table.data_ptr(),
-                           n, pages)
-    _launch(device, lib().arops_shared_prefix_attention, q.data_ptr(), stride, out.data_ptr(),
-            cache, batch, groups, options, q.shape[1], workspace.data_ptr(), workspace.nbytes)
+    groups = _pack(_pack_groups, group_start.data_ptr(), prefix_lens.data_ptr(),
+                   prefix_table.data_ptr(), n, pages)
+    _launch(device, _shared_call, q.data_ptr(), stride, out.data_ptr(), cache, batch, groups,
+            options, q.shape[1], workspace.data_ptr(), workspace.nbytes)
     return out
 
 

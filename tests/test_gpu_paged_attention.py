@@ -263,6 +263,15 @@ def test_what_lies_behind_a_length_changes_no_bit(new, lens, opt):
         assert torch.equal(run(b, pools=pools, **opt), first), f"{value} behind"
 
 
+def test_numbers_that_a_field_cannot_hold_are_refused():
+    """2^32 + 5 must not come out as a window of 5."""
+    b = Batch([1], [20], 16, 8, 128, 16, "bf16", seed=88)
+    for bad in (dict(window=2 ** 32 + 5), dict(window=-(2 ** 31) - 1), dict(window=2.5),
+                dict(softcap=1e300), dict(scale="a")):
+        with pytest.raises((ValueError, ops.ArOpsError)):
+            run(b, **bad)
+
+
 def test_very_wide_tables():
     """Tables for more positions than the tile kernel takes, and one for exactly as many."""
     for pages in (2 ** 16, 2 ** 16 + 1):

@@ -188,3 +188,17 @@ def test_binding_token_strides():
     assert ops._token_stride("q", torch.zeros(3, 16, 128)) == 2048
     assert ops._token_stride("q", torch.zeros(3, 5000)[:, :2048].unflatten(1, (16, 128))) == 5000
     assert ops._token_stride("q", torch.zeros(1, 16, 128).expand(1, 16, 128)) == 2048
+
+
+def test_packed_structures_have_the_layout_of_the_structures():
+    for make, cls, values in (
+            (ops._pack_cache, _PagedCache, (P, 2 * P, 10, 16, 8, 128, 1)),
+            (ops._pack_batch, _PagedBatch, (P, 0, 3 * P, 7, 4)),
+            (ops._pack_options, _AttentionOptions, (0.5, 20.0, 300, P, 0)),
+            (ops._pack_groups, _PrefixGroups, (P, 2 * P, 3 * P, 5, 6))):
+        expected = cls(*[v or None if n in ("kv_lens", "bidir_lens") else v
+                         for v, (n, _) in zip(values, cls._fields_)])
+        assert len(make(*values)) == C.sizeof(cls)
+        back = cls.from_buffer_copy(make(*values))
+        for name, _ in cls._fields_:
+            assert getattr(back, name) == getattr(expected, name)

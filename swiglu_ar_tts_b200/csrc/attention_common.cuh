@@ -35,18 +35,38 @@ __device__ __forceinline__ float part_factor(float mx, float m)
     return mx == -INFINITY ? 0.0f : exp2_fast(mx - m);
 }
 
-// s / cap through tanh, times cap: tanh(x) = 1 - 2 / (1 + e^2x).  Its absolute
-// error is a few 2^-24 of cap whatever x is, which is what a score needs (the
-// quotient is 0 where e^2x overflows).
-__device__ __forceinline__ float soft_cap(float s, float cap, float inv_cap)
+// cap * tanh(s / cap).  A cap may be far above the scores (a large one means
+// none), so the error goes by the score, not by the cap:
+//   |s| <= cap / 2: s (1 + y Q(y)), y = (s / cap)^2, Q of degree 3 with the least
+//   largest relative error of the whole (1.5e-8; Lawson's iteration on Chebyshev
+//   nodes): with its roundings 7.5e-8 of the result at most (2.7e-8 rms), and s
+//   itself where the cap is far away.
+//   Above: 1 - 2 / (1 + e^2|x|), a few 2^-24 of the cap, of which the result is 0.46
+//   at least.  (Taken for every score, as it was, it left decode scores of size 2
+//   an error of 2.5e-6 at cap 50, 0.46 at cap 1e7.)
+// A NaN stays one; where e^2|x| overflows the quotient is 0.
+constexpr float kCap1 = -0.33333144f, kCap2 = 0.13325879f, kCap3 = -0.053045493f,
+                kCap4 = 0.017241491f;
+
+__device__ __forceinline__ float soft_cap_large(float s, float cap, float inv_cap)
 {
-    const float e = exp2_fast(s * inv_cap * (2.0f * kLog2e));
-    return cap - 2.0f * cap * reciprocal_fast(1.0f + e);
+    const float e = exp2_fast(fabsf(s) * inv_cap * (2.0f * kLog2e));
+    return copysignf(cap * fmaf(-2.0f, reciprocal_fast(1.0f + e), 1.0f), s);
 }
 
-// tanh(x) = x P(x^2) for |x| <= 1/2, P of degree 3 with the least largest
-// relative error (5.4e-7; Lawson's iteration on Chebyshev nodes).  That is 2^-21
-// of the cap at most, the size of the other roundings of a score.
+__device__ __forceinline__ float soft_cap(float s, float cap, float inv_cap)
+{
+    const float x = s * inv_cap;
+    if (!(fabsf(x) <= 0.5f))
+        return soft_cap_large(s, cap, inv_cap);
+    const float y = x * x;
+    return fmaf(s, fmaf(fmaf(fmaf(kCap4, y, kCap3), y, kCap2), y, kCap1) * y, s);
+}
+
+// The tile kernel's form of it, for bf16: tanh(x) = x P(x^2) for |x| <= 1/2, P of
+// degree 3 with the least largest relative error (5.4e-7; as above), its
+// coefficients multiplied by what scores are multiplied by anyway.  That is
+// 2^-20 of a score with its roundings.
 constexpr float kTanh0 = 0.99999946f, kTanh1 = -0.33326319f, kTanh2 = 0.13190296f,
                 kTanh3 = -0.044402227f;
 

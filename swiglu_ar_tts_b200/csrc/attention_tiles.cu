@@ -769,8 +769,8 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                                         p.max_pages * p.map.page_size, ignore);
             } else {
                 pos = t.len - t.ntok + (int32_t)r.tok;
-                // (nobody reads a row that does not exist, but it has a vote in
-                // the scaling of its warp's sums: no keys behind the length)
+                // (nobody reads a row that does not exist, whatever query lies there;
+                // no keys behind the length for it, so that masking stays rare)
                 if (valid)
                     visible_keys(pos, t.len, t.bidir, p.window, lo, hi);
             }
@@ -813,12 +813,16 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                                       __uint_as_float(s[e + 4 + x]));
                 const float mu = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
 
-                // scale what there is only when a maximum has grown by 2^8
+                // scale what there is only when a maximum has grown by 2^8; rows
+                // beside the one that has grown keep theirs (a factor of 1), so
+                // that a row's bits depend on no other row's query
                 const bool grown = mu > m + 8.0f || (m == -INFINITY && mu > -INFINITY);
                 if (__any_sync(0xFFFFFFFFu, grown)) {
-                    const float mn = fmaxf(m, mu);
-                    const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
-                    m = mn;
+                    float f = 1.0f;
+                    if (grown) {
+                        f = m == -INFINITY ? 0.0f : exp2_fast(m - mu);
+                        m = mu;
+                    }
                     l *= f;
                     if (h > 0 || n < b - a) {
                         if (!wait(&sh.o_done[w][h ^ 1], h > 0 ? on & 1 : (on - 1) & 1))

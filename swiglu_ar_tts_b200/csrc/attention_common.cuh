@@ -54,13 +54,22 @@ __device__ __forceinline__ float soft_cap_large(float s, float cap, float inv_ca
     return copysignf(cap * fmaf(-2.0f, reciprocal_fast(1.0f + e), 1.0f), s);
 }
 
+// Whether the form above is the score's.
+__device__ __forceinline__ bool cap_is_near(float s, float inv_cap)
+{
+    return !(fabsf(s * inv_cap) <= 0.5f);
+}
+
+__device__ __forceinline__ float soft_cap_small(float s, float inv_cap)
+{
+    const float x = s * inv_cap, y = x * x;
+    return fmaf(s, fmaf(fmaf(fmaf(kCap4, y, kCap3), y, kCap2), y, kCap1) * y, s);
+}
+
 __device__ __forceinline__ float soft_cap(float s, float cap, float inv_cap)
 {
-    const float x = s * inv_cap;
-    if (!(fabsf(x) <= 0.5f))
-        return soft_cap_large(s, cap, inv_cap);
-    const float y = x * x;
-    return fmaf(s, fmaf(fmaf(fmaf(kCap4, y, kCap3), y, kCap2), y, kCap1) * y, s);
+    const float small = soft_cap_small(s, inv_cap), large = soft_cap_large(s, cap, inv_cap);
+    return cap_is_near(s, inv_cap) ? large : small;
 }
 
 // The tile kernel's form of it, for bf16: tanh(x) = x P(x^2) for |x| <= 1/2, P of
@@ -87,17 +96,49 @@ inline ScoreMap make_score_map(const AttentionParams& p)
     return m;
 }
 
+// The scores of a lane from its products, in base 2: slope[e >> 1], i[e >> 1] and
+// j0 + 8 t + (e & 1) are the bias's factor, the query's and the key's position.
+// All lanes of the warp take part: it computes the cap's second form only where
+// one of its scores needs it (256 sequences of 60-4,100 keys under a cap: 341 us,
+// 357 where all need it; 366 and 393 with a branch a score).
 template <bool FULL>
-__device__ __forceinline__ float map_score(float s, const ScoreMap& m, float slope, int32_t i,
-                                           int32_t j)
+__device__ __forceinline__ void map_scores(float (&s)[2][4], const ScoreMap& m, const float* slope,
+                                           const int32_t* i, int32_t j0)
 {
-    if constexpr (!FULL) {
-        return s * m.scale;
-    } else {
-        s *= m.scale;
-        if (m.cap > 0.0f)
-            s = soft_cap(s, m.cap, m.inv_cap);
-        return (s - slope * fabsf((float)(i - j))) * kLog2e;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s[t][e] *= m.scale;
+    if constexpr (FULL) {
+        if (m.cap > 0.0f) {
+            bool near = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    near = near || cap_is_near(s[t][e], m.inv_cap);
+            if (__any_sync(0xFFFFFFFFu, near)) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[t][e] = soft_cap(s[t][e], m.cap, m.inv_cap);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[t][e] = soft_cap_small(s[t][e], m.inv_cap);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int32_t j = j0 + t * 8 + (e & 1);
+                s[t][e] = (s[t][e] - slope[e >> 1] * fabsf((float)(i[e >> 1] - j))) * kLog2e;
+            }
     }
 }
 

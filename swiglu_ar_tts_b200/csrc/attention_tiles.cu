@@ -39,6 +39,8 @@
 // The line of units is cut into equal shares, as in the row kernel; partial
 // results go through the workspace and attention_join_kernel, launched behind,
 // joins them in the order of the keys.  Every wait is bounded in time.
+#include <float.h>
+
 #include "attention_common.cuh"
 #include "tcgen05.cuh"
 
@@ -82,8 +84,37 @@ struct TileSplit {
     int32_t tok0, ntok, sub, kvh, cta1;
 };
 
+// The cap's polynomial on raw products, in base 2: x P(x^2) with scale, cap and
+// base in the coefficients.  |score| / cap is |product| * caps.  Where the cap is
+// so far below the scale that the coefficients would overflow, products are
+// taken times `unit` first (1 otherwise).
+struct CapForm {
+    float c[4];
+    float caps, unit;
+};
+
+CapForm make_cap_form(const ScoreMap& m)
+{
+    CapForm f = {};
+    float in = fmaxf(fminf(m.scale * m.inv_cap, FLT_MAX), -FLT_MAX), out = m.scale * kLog2e;
+    f.caps = fabsf(in);
+    f.unit = 1.0f;
+    if (f.caps >= 1e5f) {
+        f.unit = in;
+        in = 1.0f;
+        out = m.cap * kLog2e;
+    }
+    const float in2 = in * in;
+    f.c[0] = kTanh0 * out;
+    f.c[1] = kTanh1 * out * in2;
+    f.c[2] = kTanh2 * out * (in2 * in2);
+    f.c[3] = kTanh3 * out * (in2 * in2 * in2);
+    return f;
+}
+
 struct TilePlan {
     ScoreMap score;
+    CapForm cap;
     TileSplit* splits;  // one a CTA
     float* parts;
     float* prefix_o;    // shared prefixes: results go here, not to out
@@ -373,7 +404,7 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                 if (!ok)
                     break;
                 unsigned char* dst = slots + s * R::kSlot;
-                const bool clean = tail && (kv == 1 || p.softcap > 0.0f);
+                const bool clean = tail && kv == 1;
                 const uint32_t bar = smem_addr(clean ? &sh.tail : &sh.full[s]);
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar, R::kSlot);
@@ -387,9 +418,7 @@ __device__ void tile_load_role(const AttentionParams& p, const TilePlan& plan,
                 ++n;
                 if (clean) {
                     // slots behind the sequence's end may hold anything, and 0
-                    // times a NaN is one: their values become zeros.  With a cap
-                    // their keys do too: a warp takes the form of tanh that all
-                    // of its products allow, those of masked keys among them.
+                    // times a NaN is one: their values become zeros
                     ok = warp_wait(&sh.tail, tails & 1, &sh.stop, p.err);
                     ++tails;
                     if (!ok)
@@ -660,11 +689,15 @@ __device__ void tile_mma_role(const AttentionParams& p, const unsigned char* q,
 // Softmax (four warps a sub-tile, a row a thread).
 // ---------------------------------------------------------------------------
 // Half a unit of a row's scores from its products, in base 2: cap, then bias.
-//   |s| <= cap / 2 in all rows of the warp (a cap is there for outliers): tanh
-//   by its polynomial, on the fp32 pipe, instead of 2 exponential-unit
-//   operations a key; scale and base are in its coefficients.
+//   |s| <= cap / 2 (a cap is there for outliers): tanh by its polynomial, on the
+//   fp32 pipe, instead of 2 exponential-unit operations a key; scale and base are
+//   in its coefficients.  The form is each score's own, so no bit depends on the
+//   rows beside it; the warp skips the second one where none of its scores needs
+//   it (a chunk of 256 tokens on 12 and 21 thousand keys: 119 us, 173 where every
+//   half has such a score; a prompt of 16,384 tokens 1,408 and 2,417).
 //   Keys not behind the query: |i - j| without the absolute value, one FMA.
-__device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const ScoreMap& map,
+__device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], uint32_t s_addr,
+                                           const ScoreMap& map, const CapForm& form,
                                            float slope, int32_t gap)
 {
     auto at = [&](int i) {
@@ -675,7 +708,6 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const Score
         s[i + 1] = __float_as_uint(x.y);
     };
     auto both = [](float x) { return make_float2(x, x); };
-    const float out = map.scale * kLog2e;
     const float bias = -slope * kLog2e;
     // the bias of keys e, e + 1 (e = 0, 2, .. 14); of those 16, 32, 48 on: one
     // more addition each
@@ -687,42 +719,74 @@ __device__ __forceinline__ void map_scores(uint32_t (&s)[kHalfUnit], const Score
         for (int i = 0; i < kHalfUnit; i += 2)
             big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[i]))),
                         fabsf(__uint_as_float(s[i + 1])));
-        const float in = map.scale * map.inv_cap, in2 = in * in;
-        if (__all_sync(0xFFFFFFFFu, big * fabsf(in) <= 0.5f && fabsf(in) < 1e5f)) {
-            const float2 c0 = both(kTanh0 * out), c1 = both(kTanh1 * out * in2),
-                         c2 = both(kTanh2 * out * (in2 * in2)),
-                         c3 = both(kTanh3 * out * (in2 * in2 * in2));
-            if (behind) {
+        const float2 c0 = both(form.c[0]), c1 = both(form.c[1]), c2 = both(form.c[2]),
+                     c3 = both(form.c[3]);
+        if (__any_sync(0xFFFFFFFFu, big * form.caps > 0.5f) || form.unit != 1.0f) {
+            // both forms, 16 products at a time out of tensor memory and back (a
+            // row's 64 with two forms each do not fit the registers); the sums as
+            // below
+            float2 add[8];
 #pragma unroll
-                for (int i = 0; i < kHalfUnit; i += 2) {
-                    const float2 x = at(i);
-                    const float2 y = mul2(x, x);
-                    put(i, mul2(x, fma2(fma2(fma2(y, c3, c2), y, c1), y, c0)));
-                }
-            } else {
+            for (int e = 0; e < 16; e += 2)
+                add[e / 2] = behind ? both(0.0f)
+                                    : make_float2(bias * (float)(gap - e),
+                                                  bias * (float)(gap - e - 1));
+#pragma unroll 1
+            for (int c = 0; c < kHalfUnit; c += 16) {
+                uint32_t raw[16];
+                tc_load16(raw, s_addr + c);
+                tc_wait_ld();
+                tc_loaded<16>(raw);
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                    float2 add = make_float2(bias * (float)(gap - e), bias * (float)(gap - e - 1));
-#pragma unroll
-                    for (int i = e; i < kHalfUnit; i += 16) {
-                        const float2 x = at(i);
-                        const float2 y = mul2(x, x);
-                        put(i, fma2(x, fma2(fma2(fma2(y, c3, c2), y, c1), y, c0), add));
-                        add = add2(add, step);
-                    }
+                    const float2 p =
+                        make_float2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1]));
+                    const float2 x = mul2(p, both(form.unit));
+                    const float2 y = mul2(x, x);
+                    float2 r = fma2(x, fma2(fma2(fma2(y, c3, c2), y, c1), y, c0), add[e / 2]);
+                    const float fx = soft_cap_large(p.x * map.scale, map.cap, map.inv_cap);
+                    const float fy = soft_cap_large(p.y * map.scale, map.cap, map.inv_cap);
+                    r.x = fabsf(p.x) * form.caps > 0.5f ? fmaf(fx, kLog2e, add[e / 2].x) : r.x;
+                    r.y = fabsf(p.y) * form.caps > 0.5f ? fmaf(fy, kLog2e, add[e / 2].y) : r.y;
+                    raw[e] = __float_as_uint(r.x);
+                    raw[e + 1] = __float_as_uint(r.y);
+                    if (!behind)
+                        add[e / 2] = add2(add[e / 2], step);
                 }
-                return;
+                tc_store16(s_addr + c, raw);
+            }
+            tc_wait_st();
+            tc_load32(s, s_addr);
+            tc_load32(s + 32, s_addr + 32);
+            tc_wait_ld();
+            tc_loaded<kHalfUnit>(s);
+        } else if (behind) {
+#pragma unroll
+            for (int i = 0; i < kHalfUnit; i += 2) {
+                const float2 x = at(i);
+                const float2 y = mul2(x, x);
+                put(i, mul2(x, fma2(fma2(fma2(y, c3, c2), y, c1), y, c0)));
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < kHalfUnit; ++i)
-                s[i] = __float_as_uint(
-                    soft_cap(__uint_as_float(s[i]) * map.scale, map.cap, map.inv_cap) * kLog2e);
+            for (int e = 0; e < 16; e += 2) {
+                float2 add = make_float2(bias * (float)(gap - e), bias * (float)(gap - e - 1));
+#pragma unroll
+                for (int i = e; i < kHalfUnit; i += 16) {
+                    const float2 x = at(i);
+                    const float2 y = mul2(x, x);
+                    put(i, fma2(x, fma2(fma2(fma2(y, c3, c2), y, c1), y, c0), add));
+                    add = add2(add, step);
+                }
+            }
         }
+        if (!behind)
+            return;
     } else {
+        const float2 out = both(map.scale * kLog2e);
 #pragma unroll
         for (int i = 0; i < kHalfUnit; i += 2)
-            put(i, mul2(at(i), both(out)));
+            put(i, mul2(at(i), out));
     }
     if (__all_sync(0xFFFFFFFFu, slope == 0.0f))
         return;
@@ -794,7 +858,7 @@ __device__ void tile_softmax_role(const AttentionParams& p, const TilePlan& plan
                 tc_wait_ld();
                 tc_loaded<kHalfUnit>(s);
                 if constexpr (FULL)
-                    map_scores(s, plan.score, slope, pos - key0);
+                    map_scores(s, s_addr, plan.score, plan.cap, slope, pos - key0);
                 if (__any_sync(0xFFFFFFFFu, key0 < lo || hi - key0 < kHalfUnit)) {
                     const int32_t first = lo - key0, last = hi - key0;
 #pragma unroll
@@ -1445,6 +1509,7 @@ cudaError_t launch_attention_tiles(const AttentionParams& p, float* parts, float
     plan.score = make_score_map(p);
     if (full)
         plan.score.scale = p.scale;
+    plan.cap = make_cap_form(plan.score);
     plan.parts = parts;
     plan.splits = reinterpret_cast<TileSplit*>(
         parts + (size_t)kMaxTileCtas * 4 * tile_part_floats(p.head_dim <= 64 ? 64 : 128));

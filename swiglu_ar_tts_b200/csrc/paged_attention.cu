@@ -945,6 +945,7 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
             }
 
             // softmax: what a row does not see is -inf
+            map_scores<FULL>(s, plan.score, slope, pos, b.key0 + b.shift + 2 * quad);
             const int32_t end = b.end + b.shift;
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -956,8 +957,7 @@ attention_rows_kernel(const __grid_constant__ AttentionParams p,
                     bool seen = j >= lo[i] && j < min(hi[i], end);
                     if (SHARED && b.member >= 0)
                         seen = seen && member[i] == b.member;
-                    s[t][e] = seen ? map_score<FULL>(s[t][e], plan.score, slope[i], pos[i], j)
-                                   : -INFINITY;
+                    s[t][e] = seen ? s[t][e] : -INFINITY;
                     mx[i] = fmaxf(mx[i], s[t][e]);
                 }
             float f[2];

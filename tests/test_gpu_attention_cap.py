@@ -120,3 +120,15 @@ def test_a_cap_far_above_the_scores_is_no_cap():
             # of up to 20 that differ by four roundings
             limit = 2.0 ** -6 if dtype == "bf16" else 2 * 300 * 2.0 ** -23 + 2 * 20 * 2.0 ** -22
             assert float((x - y).abs().max()) <= limit * float(dev(b.v_pages).nan_to_num().abs().max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,lens,page", SHAPES)
+@pytest.mark.parametrize("biased", [False, True])
+def test_a_cap_far_below_the_scale(new, lens, page, biased, dtype):
+    """Queries 2^24 times smaller under a scale 2^24 times larger: the same scores
+    and cap, but for a polynomial on the products themselves nothing is left."""
+    b = Batch(new, lens, 8, 4, 128, page, dtype, seed=99, q_std=4.0)
+    opt = dict(softcap=6.0, **({"slopes": _slopes(8)} if biased else {}))
+    got = run(b, q=dev(b.q) * 2.0 ** -24, scale=2.0 ** 24 * 128 ** -0.5, **opt)
+    check(b, got, 6.0, opt.get("slopes"), f"far below {dtype} {new}")

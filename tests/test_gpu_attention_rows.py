@@ -11,7 +11,7 @@ from tolerance import to_f64
 
 pytestmark = pytest.mark.gpu
 
-OPTS = [{}, {"slopes": _slopes(16)}]
+OPTS = [{}, {"softcap": 20.0}, {"softcap": 3.0, "slopes": _slopes(16)}, {"slopes": _slopes(16)}]
 VALUES = [0.0, 30.0, -1e4, float("inf"), float("nan")]
 
 

@@ -514,6 +514,14 @@ def attention_prepare(workspace: torch.Tensor) -> torch.Tensor:
     return workspace
 
 
+def _options(scale, softcap, window, slopes: int, bidir_lens: int) -> bytes:
+    """arops_attention_options; a cap that is no longer one as a float is refused."""
+    packed = _pack(_pack_options, scale, softcap, window, slopes, bidir_lens)
+    if softcap != 0 and abs(softcap) < 2.0 ** -149:
+        raise ValueError(f"softcap {softcap} is 0, which is no cap, as a float")
+    return packed
+
+
 def _attention_args(q, k_pages, v_pages, q_start, kv_lens, block_table, scale, softcap, window,
                     slopes, bidir_lens, workspace, out):
     """Checks and arguments that both attention operators share (q_start: None
@@ -539,8 +547,7 @@ def _attention_args(q, k_pages, v_pages, q_start, kv_lens, block_table, scale, s
     if bidir_lens is not None:
         _need("bidir_lens", bidir_lens, device, torch.int32, (n,))
         bidir_ptr = bidir_lens.data_ptr()
-    options = _pack(_pack_options, d ** -0.5 if scale is None else scale, softcap, window,
-                    slope_ptr, bidir_ptr)
+    options = _options(d ** -0.5 if scale is None else scale, softcap, window, slope_ptr, bidir_ptr)
     batch = _pack(_pack_batch, starts, kv_lens.data_ptr(), block_table.data_ptr(), n, pages)
     if workspace is None:
         workspace = attention_prepare(torch.empty(attention_workspace(tokens, hq, d),

@@ -1,0 +1,20 @@
+"""Numbers that the paged-cache binding must not change on their way to the
+library (no GPU needed)."""
+import pytest
+
+import swiglu_ar_tts_b200 as ops
+
+
+@pytest.mark.parametrize("cap", [1e-50, -1e-50, 1e-46, 5e-324, 2.0 ** -150])
+def test_a_cap_that_vanishes_as_a_float_is_refused(cap):
+    """1e-50 must not come out as 0, which is no cap at all."""
+    with pytest.raises(ValueError):
+        ops._options(0.1, cap, 0, 0, 0)
+
+
+def test_caps_that_a_float_holds():
+    for cap in (0.0, 0, -0.0):
+        assert ops._options(0.1, cap, 0, 0, 0) == ops._pack_options(0.1, cap, 0, 0, 0)
+    # these are the library's to refuse or to take
+    for cap in (2.0 ** -149, 1e-30, 30, 30.0, 3e38, -1.0, float("nan"), float("inf")):
+        assert ops._options(0.1, cap, 5, 8, 16) == ops._pack_options(0.1, cap, 5, 8, 16)

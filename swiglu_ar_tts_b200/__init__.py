@@ -73,7 +73,8 @@ _pack_cache = struct.Struct("@PPqiiii").pack
 _pack_batch = struct.Struct("@PPPii").pack
 _pack_options = struct.Struct("@ffiPP").pack
 _pack_groups = struct.Struct("@PPPii").pack
-_Sections = _i32 * 3
+_pack_sections = struct.Struct("@iii").pack
+_pack_sizes = struct.Struct("@qii").pack
 _append_call = _attention_call = _shared_call = None  # set by lib()
 
 
@@ -140,8 +141,7 @@ def lib() -> ctypes.CDLL:
                    "arops_attention_prepare", "arops_paged_attention",
                    "arops_shared_prefix_attention"):
             getattr(L, fn).restype = ctypes.c_int
-        packed = {cache: ctypes.c_char_p, batch: ctypes.c_char_p, options: ctypes.c_char_p,
-                  groups: ctypes.c_char_p}
+        packed = {t: ctypes.c_char_p for t in (cache, batch, options, groups, ctypes.POINTER(_i32))}
 
         def with_bytes(name):
             fn = L[name]  # a function object of its own
@@ -491,7 +491,7 @@ def mrope_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: t
     lib()
     _launch(device, _append_call, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
             q_out.data_ptr(), so, cache, batch, gq, gk, eps, pos.data_ptr(), tokens, hq,
-            _Sections(*sections), theta)
+            _pack(_pack_sections, *sections), theta)
     return q_out
 
 
@@ -499,6 +499,7 @@ def attention_workspace(tokens: int, n_q_heads: int, head_dim: int) -> int:
     """Bytes of device workspace that paged_attention and
     shared_prefix_attention need for this many query tokens."""
     n = ctypes.c_size_t(0)
+    _pack(_pack_sizes, tokens, n_q_heads, head_dim)  # ctypes would cut them to their bits
     _check(lib().arops_attention_workspace(tokens, n_q_heads, head_dim, ctypes.byref(n)))
     return int(n.value)
 

@@ -18,3 +18,20 @@ def test_caps_that_a_float_holds():
     # these are the library's to refuse or to take
     for cap in (2.0 ** -149, 1e-30, 30, 30.0, 3e38, -1.0, float("nan"), float("inf")):
         assert ops._options(0.1, cap, 5, 8, 16) == ops._pack_options(0.1, cap, 5, 8, 16)
+
+
+@pytest.mark.parametrize("sizes", [(2 ** 64 + 5, 16, 128), (5, 2 ** 32 + 16, 128), (5, 16, 2 ** 32 + 128),
+                                   (-(2 ** 63) - 1, 16, 128), (5.5, 16, 128)])
+def test_workspace_sizes_that_a_field_cannot_hold(sizes):
+    """2^32 + 16 heads must not come out as the workspace of 16."""
+    with pytest.raises(ValueError):
+        ops.attention_workspace(*sizes)
+    assert ops.attention_workspace(5, 16, 128) > 0
+
+
+@pytest.mark.parametrize("sections", [(2 ** 32 + 24, 20, 20), (24, 20, 20 - 2 ** 32), (24, 40), (24, 20, 10, 10),
+                                      (24.5, 20, 19)])
+def test_sections_that_a_field_cannot_hold(sections):
+    with pytest.raises(ValueError):
+        ops._pack(ops._pack_sections, *sections)
+    assert ops._pack(ops._pack_sections, 24, 20, 20) == bytes((ops._i32 * 3)(24, 20, 20))

@@ -286,8 +286,12 @@ typedef struct {
  * pages that it does not name, never reach the result, whatever they hold;
  * values inside the length are expected to be finite (a NaN or an infinity
  * there may reach queries that do not see it).
- *   workspace   device scratch of at least arops_attention_workspace() bytes
- *               (16-byte aligned, caller-owned).  It starts with 16 KiB of
+ *   workspace   device scratch (16-byte aligned, caller-owned) of at least
+ *               arops_attention_workspace() bytes, which serve either attention
+ *               operator, or of arops_paged_attention_workspace() bytes, which
+ *               serve this one alone (it has no use for a prefix's results:
+ *               4 * tokens * n_q_heads * (head_dim + 2) bytes, head_dim rounded
+ *               up to 64 or 128, where there are any).  It starts with 16 KiB of
  *               arrival counters that must be zero when a call begins: clear
  *               them once, with arops_attention_prepare; every call leaves them
  *               zero again, for any later call of either attention operator.
@@ -300,6 +304,8 @@ typedef struct {
  */
 AROPS_API arops_status arops_attention_workspace(int64_t tokens, int32_t n_q_heads,
                                                  int32_t head_dim, size_t* bytes);
+AROPS_API arops_status arops_paged_attention_workspace(int64_t tokens, int32_t n_q_heads,
+                                                       int32_t head_dim, size_t* bytes);
 AROPS_API arops_status arops_attention_prepare(void* workspace, size_t workspace_bytes,
                                                void* stream);
 AROPS_API arops_status arops_paged_attention(const void* q, int64_t q_stride, void* out,

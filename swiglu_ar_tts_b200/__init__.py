@@ -132,14 +132,15 @@ def lib() -> ctypes.CDLL:
                                                batch, _vp, _vp, ctypes.c_float, _vp, _i64, _i32,
                                                ctypes.POINTER(_i32), ctypes.c_float, _vp]
         L.arops_attention_workspace.argtypes = [_i64, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
+        L.arops_paged_attention_workspace.argtypes = L.arops_attention_workspace.argtypes
         L.arops_attention_prepare.argtypes = [_vp, ctypes.c_size_t, _vp]
         L.arops_paged_attention.argtypes = [_vp, _i64, _vp, cache, batch, options, _i64, _i32, _vp,
                                             ctypes.c_size_t, _vp]
         L.arops_shared_prefix_attention.argtypes = [_vp, _i64, _vp, cache, batch, groups, options,
                                                     _i32, _vp, ctypes.c_size_t, _vp]
         for fn in ("arops_mrope_paged_append", "arops_attention_workspace",
-                   "arops_attention_prepare", "arops_paged_attention",
-                   "arops_shared_prefix_attention"):
+                   "arops_paged_attention_workspace", "arops_attention_prepare",
+                   "arops_paged_attention", "arops_shared_prefix_attention"):
             getattr(L, fn).restype = ctypes.c_int
         packed = {t: ctypes.c_char_p for t in (cache, batch, options, groups, ctypes.POINTER(_i32))}
 
@@ -495,12 +496,15 @@ def mrope_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: t
     return q_out
 
 
-def attention_workspace(tokens: int, n_q_heads: int, head_dim: int) -> int:
+def attention_workspace(tokens: int, n_q_heads: int, head_dim: int,
+                        shared_prefix: bool = True) -> int:
     """Bytes of device workspace that paged_attention and
-    shared_prefix_attention need for this many query tokens."""
+    shared_prefix_attention need for this many query tokens; paged_attention
+    alone (``shared_prefix=False``) needs fewer where there are many."""
     n = ctypes.c_size_t(0)
     _pack(_pack_sizes, tokens, n_q_heads, head_dim)  # ctypes would cut them to their bits
-    _check(lib().arops_attention_workspace(tokens, n_q_heads, head_dim, ctypes.byref(n)))
+    fn = lib().arops_attention_workspace if shared_prefix else lib().arops_paged_attention_workspace
+    _check(fn(tokens, n_q_heads, head_dim, ctypes.byref(n)))
     return int(n.value)
 
 
@@ -551,8 +555,8 @@ def _attention_args(q, k_pages, v_pages, q_start, kv_lens, block_table, scale, s
     options = _options(d ** -0.5 if scale is None else scale, softcap, window, slope_ptr, bidir_ptr)
     batch = _pack(_pack_batch, starts, kv_lens.data_ptr(), block_table.data_ptr(), n, pages)
     if workspace is None:
-        workspace = attention_prepare(torch.empty(attention_workspace(tokens, hq, d),
-                                                  dtype=torch.uint8, device=q.device))
+        size = attention_workspace(tokens, hq, d, shared_prefix=q_start is None)
+        workspace = attention_prepare(torch.empty(size, dtype=torch.uint8, device=q.device))
     elif workspace.get_device() != device or not workspace.is_contiguous():
         _reject("workspace", workspace, device, workspace.dtype, None)
     lib()
@@ -572,8 +576,9 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     of the sequence's queries; ``window`` > 0 hides keys that far back;
     ``softcap`` > 0 caps scores by a tanh; ``slopes`` [Hq] subtracts
     slope * distance.  ``scale`` defaults to D ** -0.5.  ``workspace`` is a
-    uint8 tensor of attention_workspace() bytes, cleared once
-    (attention_prepare); allocated and cleared here if omitted."""
+    uint8 tensor of attention_workspace() bytes (``shared_prefix=False`` is
+    enough here), cleared once (attention_prepare); allocated and cleared here
+    if omitted."""
     device, stride, cache, batch, options, workspace, out = _attention_args(
         q, k_pages, v_pages, q_start, kv_lens, block_table, scale, softcap, window, slopes,
         bidir_lens, workspace, out)

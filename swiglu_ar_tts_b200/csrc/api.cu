@@ -347,6 +347,21 @@ arops_status check_workspace(const char* name, const void* workspace, size_t byt
     return AROPS_OK;
 }
 
+arops_status workspace_entry(const char* name, int64_t tokens, int32_t n_q_heads,
+                             int32_t head_dim, bool shared_prefix, size_t* bytes)
+{
+    if (!bytes)
+        return fail(AROPS_ERR_INVALID, "%s: bytes is null", name);
+    if (tokens < 0 || n_q_heads < 1 || head_dim < 1)
+        return fail(AROPS_ERR_INVALID, "%s: bad shape tokens=%lld n_q_heads=%d head_dim=%d", name,
+                    (long long)tokens, (int)n_q_heads, (int)head_dim);
+    if (tokens > INT32_MAX || n_q_heads > 65535 || head_dim > 256)
+        return fail(AROPS_ERR_UNSUPPORTED,
+                    "%s: supported tokens < 2^31, n_q_heads <= 65535, head_dim <= 256", name);
+    *bytes = attention_workspace_bytes(tokens, n_q_heads, head_dim, shared_prefix);
+    return ok();
+}
+
 // The checks and the launch that the two attention operators share.
 arops_status attention_entry(const char* name, const void* q, int64_t q_stride, void* out,
                              const arops_paged_cache* cache, const arops_paged_batch* batch,
@@ -407,7 +422,8 @@ arops_status attention_entry(const char* name, const void* q, int64_t q_stride, 
     if (q == out)
         return fail(AROPS_ERR_INVALID, "%s: q and out are one buffer", name);
     st = check_workspace(name, workspace, workspace_bytes,
-                         attention_workspace_bytes(tokens, n_q_heads, cache->head_dim));
+                         attention_workspace_bytes(tokens, n_q_heads, cache->head_dim,
+                                                   groups != nullptr));
     if (st != AROPS_OK)
         return st;
     AttentionParams p = {};
@@ -525,17 +541,14 @@ AROPS_API arops_status arops_mrope_paged_append(
 AROPS_API arops_status arops_attention_workspace(int64_t tokens, int32_t n_q_heads,
                                                  int32_t head_dim, size_t* bytes)
 {
-    const char* name = "arops_attention_workspace";
-    if (!bytes)
-        return fail(AROPS_ERR_INVALID, "%s: bytes is null", name);
-    if (tokens < 0 || n_q_heads < 1 || head_dim < 1)
-        return fail(AROPS_ERR_INVALID, "%s: bad shape tokens=%lld n_q_heads=%d head_dim=%d", name,
-                    (long long)tokens, (int)n_q_heads, (int)head_dim);
-    if (tokens > INT32_MAX || n_q_heads > 65535 || head_dim > 256)
-        return fail(AROPS_ERR_UNSUPPORTED,
-                    "%s: supported tokens < 2^31, n_q_heads <= 65535, head_dim <= 256", name);
-    *bytes = attention_workspace_bytes(tokens, n_q_heads, head_dim);
-    return ok();
+    return workspace_entry("arops_attention_workspace", tokens, n_q_heads, head_dim, true, bytes);
+}
+
+AROPS_API arops_status arops_paged_attention_workspace(int64_t tokens, int32_t n_q_heads,
+                                                       int32_t head_dim, size_t* bytes)
+{
+    return workspace_entry("arops_paged_attention_workspace", tokens, n_q_heads, head_dim, false,
+                           bytes);
 }
 
 AROPS_API arops_status arops_attention_prepare(void* workspace, size_t workspace_bytes,

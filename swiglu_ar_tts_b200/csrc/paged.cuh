@@ -140,9 +140,10 @@ struct PagedAppendArgs {
 cudaError_t launch_paged_append(const PagedAppendArgs& a, arops_dtype dtype, cudaStream_t stream);
 
 // Attention (paged_attention.cu).  The workspace starts with
-// attention_counter_bytes() of arrival counters, zero between calls.
+// attention_counter_bytes() of arrival counters, zero between calls; only shared
+// prefixes have results of their own in it.
 size_t attention_counter_bytes();
-size_t attention_workspace_bytes(int64_t tokens, int hq, int head_dim);
+size_t attention_workspace_bytes(int64_t tokens, int hq, int head_dim, bool shared_prefix);
 cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* workspace,
                              cudaStream_t stream);
 

@@ -1223,15 +1223,16 @@ bool many_rows(const AttentionParams& p)
 }
 
 // The two kernels' partial results share a region: the second launch of a call
-// waits for the first.  The prefix's results of every (sequence, head) follow.
-size_t attention_workspace_bytes(int64_t tokens, int hq, int head_dim)
+// waits for the first.  With shared prefixes the prefix's results of every
+// (sequence, head) follow.
+size_t attention_workspace_bytes(int64_t tokens, int hq, int head_dim, bool shared_prefix)
 {
     const int dp = padded_head_dim(head_dim);
     size_t parts = (size_t)kMaxRowCtas * 2 * part_floats(dp) * sizeof(float);
     if (dp > 128 || tokens * hq < 96)  // too few rows for the tile kernel
         return kCounterBytes + parts;
     return kCounterBytes + std::max(parts, tile_part_bytes(dp)) +
-           (size_t)tokens * hq * (dp + 2) * sizeof(float);
+           (shared_prefix ? (size_t)tokens * hq * (dp + 2) * sizeof(float) : 0);
 }
 
 cudaError_t launch_attention(const AttentionParams& p, arops_dtype dtype, void* workspace,

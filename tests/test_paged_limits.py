@@ -1,5 +1,7 @@
 """Numbers that the paged-cache binding must not change on their way to the
 library (no GPU needed)."""
+import ctypes
+
 import pytest
 
 import swiglu_ar_tts_b200 as ops
@@ -35,3 +37,26 @@ def test_sections_that_a_field_cannot_hold(sections):
     with pytest.raises(ValueError):
         ops._pack(ops._pack_sections, *sections)
     assert ops._pack(ops._pack_sections, 24, 20, 20) == bytes((ops._i32 * 3)(24, 20, 20))
+
+
+@pytest.mark.parametrize("tokens,heads,d", [(0, 1, 1), (5, 16, 128), (16384, 16, 128), (2000, 12, 64), (300, 8, 256),
+                                            (100_000, 16, 128)])
+def test_workspace_of_one_operator(tokens, heads, d):
+    """Attention without shared prefixes keeps nothing per token: a prompt of any
+    length takes the same space."""
+    both = ops.attention_workspace(tokens, heads, d)
+    alone = ops.attention_workspace(tokens, heads, d, shared_prefix=False)
+    width = 64 if d <= 64 else 128
+    prefixes = tokens * heads * (width + 2) * 4 if d <= 128 and tokens * heads >= 96 else 0
+    assert both - alone == prefixes
+    assert 16384 < alone < 64 << 20
+
+
+def test_workspace_of_one_operator_refuses_as_the_other():
+    n = ctypes.c_size_t(0)
+    for f in (ops.lib().arops_attention_workspace, ops.lib().arops_paged_attention_workspace):
+        assert f(5, 16, 128, None) == 1
+        for bad in ((-1, 16, 128), (5, 0, 128), (5, 16, 0)):
+            assert f(*bad, ctypes.byref(n)) == 1
+        for bad in ((1 << 31, 16, 128), (5, 65536, 128), (5, 16, 257)):
+            assert f(*bad, ctypes.byref(n)) == 2

@@ -263,7 +263,7 @@ AROPS_API arops_status arops_mrope_paged_append(
  */
 typedef struct {
     float scale;               /* finite; 1/sqrt(head_dim) usually */
-    float softcap;             /* finite, >= 1e-30, or 0: no cap */
+    float softcap;             /* finite, >= 1e-30, or 0: no cap; its size costs no accuracy */
     int32_t window;            /* >= 0 positions, the query's own included; 0: no limit */
     const float* slopes;       /* [n_q_heads] float32 device array, or NULL */
     const int32_t* bidir_lens; /* [n_seqs] int32 device array, or NULL */
@@ -282,10 +282,13 @@ typedef struct {
  * Scores, softmax statistics and sums are fp32.  In bf16 the weights of the
  * second product are rounded to bf16, as q, k and v are; in fp32 both products
  * run on the tensor cores with every operand split into two tf32 parts (about
- * 21 bits).  The values of slots at and behind a sequence's length, and of
- * pages that it does not name, never reach the result, whatever they hold;
- * values inside the length are expected to be finite (a NaN or an infinity
- * there may reach queries that do not see it).
+ * 21 bits; a number within 2^-12 of the type's largest counts as not finite).
+ * The values of slots at and behind a sequence's length, and of pages that it
+ * does not name, never reach the result, whatever they hold; values inside the
+ * length are expected to be finite (a NaN or an infinity there may reach queries
+ * that do not see it).  A token's result depends on its own query, its
+ * sequence's keys and the lengths of the batch, on no other token's query:
+ * padding tokens may hold anything.
  *   workspace   device scratch (16-byte aligned, caller-owned) of at least
  *               arops_attention_workspace() bytes, which serve either attention
  *               operator, or of arops_paged_attention_workspace() bytes, which
@@ -327,7 +330,7 @@ typedef struct {
     const int32_t* group_start;  /* [n_groups + 1], non-decreasing from 0 */
     const int32_t* prefix_lens;  /* [n_groups] */
     const int32_t* prefix_table; /* [n_groups, max_prefix_pages] */
-    int32_t n_groups;
+    int32_t n_groups;            /* at most n_seqs, empty groups among them */
     int32_t max_prefix_pages;
 } arops_prefix_groups;
 

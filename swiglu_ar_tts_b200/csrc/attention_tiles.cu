@@ -27,13 +27,14 @@
 // half) is latency of the two warps that a scheduler has, and there is room for
 // no third in the registers.  Exponentials on the fp32 pipe (1/8 to 1/2 of them)
 // measured slower, and so did weights taken with the maximum before this half's.
-// One prompt of 16,384 tokens, 16 heads on 8 of 128: 886 us, 1,241 TFLOP/s (74% of
-// the measured cuBLAS rate, 88% of its rate under the power cap, which holds the
-// clocks of repeated calls down: 900-1,040 us then).
+// One prompt of 16,384 tokens, 16 heads on 8 of 128: 900 us, 1,222 TFLOP/s at full
+// clocks (73% of the measured cuBLAS rate); in repeated calls, whose clocks the
+// power cap holds down, 1,000-1,050 us (75-78% of cuBLAS's rate under it).
 //
-// O stays in tensor memory; it is scaled only when a row's maximum has grown by
-// more than 2^8 since the last time (P and l carry the factor until then; both
-// are floating point, so nothing is lost).  Tensor memory: S_0, S_1, O_0, O_1,
+// O stays in tensor memory; a row of it is scaled only when the row's maximum has
+// grown by more than 2^8 since the last time (P and l carry the factor until then;
+// both are floating point, so nothing is lost).  Nothing of a row depends on the
+// rows beside it.  Tensor memory: S_0, S_1, O_0, O_1,
 // all 512 columns, one CTA an SM.
 //
 // The line of units is cut into equal shares, as in the row kernel; partial

@@ -10,8 +10,8 @@
 // values a token and computes ~8 operations on each, so memory bounds it; a
 // decode step is bound by latency: positions, lengths and the block table form
 // a chain of three dependent loads, the activations' loads run beside it (5
-// tokens: 3.3 us a launch back to back).  A ragged batch of 7,443 tokens, 122 MB,
-// takes 28.0 us, 66% of the measured copy rate: 950 instructions a warp and half
+// tokens: 3.3-3.5 us a launch back to back).  A ragged batch of 7,443 tokens, 122 MB,
+// takes 27.1 us, 69% of the measured copy rate: 950 instructions a warp and half
 // token (angles, norms, rotation) keep half of the issue slots busy, and an SM's
 // sixteen warps do not cover the rest of each other's latencies; more warps of
 // fewer registers, weights kept in registers, or the next token's data brought

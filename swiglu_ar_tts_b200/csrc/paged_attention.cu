@@ -151,11 +151,13 @@ struct RowTraits {
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kHalf = kBlock * kRowBytes;      // a warp's keys (or values)
     static constexpr int kStage = 2 * kHalf;
-    // Stages of a warp's ring and CTAs an SM: 96 KB in flight an SM, above the
-    // ~64 KB that 44 GB/s an SM need at ~1 us of latency.  bf16 heads of 128:
-    // three CTAs of two stages, the third to fill the other two's changes of
-    // sequence; two of three stages measured 354 against 344 us (256 sequences
-    // of 60-4,100 keys), three stages being more than the loads need.
+    // Stages of a warp's ring and CTAs an SM.  A warp asks for its next stage when
+    // it has used one, so kStages - 1 of them are on their way while it waits and
+    // one fewer while it multiplies: with two stages that is none, and other
+    // warps' copies fill the time (bf16 heads of 128: at most 96 KB an SM, above
+    // the ~64 KB that 44 GB/s an SM need at ~1 us of latency).  Three CTAs of two
+    // stages, the third to fill the other two's changes of sequence, measured 344
+    // us against 354 for two of three (256 sequences of 60-4,100 keys).
     static constexpr int kStages = kStage == 8192 ? 2 : 3;
     static constexpr int kCtas = kStage <= 4096 ? 4 : kStage <= 8192 ? 3 : 1;
     static constexpr int kSteps = kE == 2 ? DP / 16 : DP / 8;  // of the first product
@@ -1205,15 +1207,18 @@ size_t attention_counter_bytes()
 }
 
 // Which calls go to the tile kernel, by their rows (tokens times query heads a
-// key head).  It takes ~35 us whatever it does and passes over the keys once for
-// up to 256 rows; the row kernel passes over them once for 16.
+// key head).  It passes over the keys once for up to 256 rows, the row kernel
+// once for 16; its fixed cost is the higher one (a prompt of 60 tokens: row 7.9
+// against tile 13.6 us; 200: 16.9 / 17.4; 400: 31.9 / 19.1; 1,000: 65 / 26).
 //   Ragged batches (rows a sequence, row against tile kernel): 64 sequences on
-//   1,000 positions 16: 61 against 75 us, 24: 103 / 74, 64: 189 / 83; 8 on 4,000
-//   16: 38 / 47, 24: 54 / 47; 200 on 300 16: 73 / 86, 24: 115 / 87; but one on
-//   8,000 64: 34 / 36, 96: 39 / 37.
-//   Prefixes (rows a group): 8 groups on 2,000 positions 48: 64 / 66, 64: 79 / 71,
-//   128: 131 / 94; 20 on 500 64: 92 / 99, 128: 160 / 153; but one on 2,000 128:
-//   30 / 50.
+//   1,000 positions 16: 62 against 76 us, 24: 103 / 76; 8 on 4,000 16: 38 / 47,
+//   24: 54 / 47; 200 on 300 16: 72 / 87, 24: 115 / 88; one on 8,000 96: 43 / 37.
+//   Prefixes (rows a group): 8 groups on 2,000 positions 48: 78 / 82, 64: 95 / 90,
+//   128: 164 / 129; one on 2,000 128: 37 / 57, 510: 93 / 85.
+// The rule sees the call's rows alone, and one kernel takes all of it.  So the
+// shortest prompts lose up to 6 us, 20 groups of 64 rows on 500 positions 7 (134 /
+// 141), and a call of decode steps and prompts pays for the side that is in the
+// minority (255 steps and a prompt of 1,500 tokens: 271 us; apart 185 and 33).
 bool many_rows(const AttentionParams& p)
 {
     const int64_t rows = p.tokens * (p.hq / p.hk);
